@@ -1,4 +1,5 @@
-"""ctypes binding of libbq.so -- same names as the C ABI in include/bq.h.
+"""ctypes binding of libbq.so -- same names as the C ABI in include/bq.h and
+include/bq_kv.h.
 
 Argument marshalling only: every step of the GEMV runs in the CUDA library.
 The raw functions take integer addresses (device or host, as the header says)
@@ -19,6 +20,9 @@ BQ_OK, BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_BATCH = 0, 1, 2, 3, 4
 BQ_ERR_EXPERT_INDEX, BQ_ERR_CUDA, BQ_ERR_TIMEOUT, BQ_ERR_WORKSPACE, BQ_ERR_RANGE = 5, 6, 7, 8, 9
 BQ_EPI_NONE, BQ_EPI_SWIGLU = 0, 1
 BQ_GEMV_STATIC_WEIGHTS, BQ_GEMV_ROWS16, BQ_GEMV_ROWS32 = 1, 2, 4
+# include/bq_kv.h
+BQ_ERR_POSITION = 10
+BQ_F32, BQ_F16, BQ_BF16 = 0, 1, 2
 
 
 class bq_qmat(ctypes.Structure):
@@ -49,6 +53,19 @@ class bq_kv_cache(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("vt_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
                 ("D", ctypes.c_int32), ("Tmax", ctypes.c_int32)]
+
+
+class bq_kv_cache_q4(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("D", ctypes.c_int32), ("Tmax", ctypes.c_int32)]
+
+
+class bq_kv_rows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_batch", ctypes.c_int64), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_batch", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("T", ctypes.c_int32)]
 
 
 class bq_gemv_geometry(ctypes.Structure):
@@ -119,6 +136,19 @@ _SIGS = {
     "bq_quantize_q5_dev": (_i32, [_vp, _i32, _i32, _vp, _vp, _vp, _vp]),
 }
 
+# name -> (restype, argtypes); mirrors include/bq_kv.h
+_KVP, _KV4P = ctypes.POINTER(bq_kv_cache), ctypes.POINTER(bq_kv_cache_q4)
+_RWP = ctypes.POINTER(bq_kv_rows)
+_KV_SIGS = {
+    "bq_kv_append_q4": (_i32, [_KV4P, _RWP, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "bq_kv_append_q8": (_i32, [_KVP, _RWP, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "bq_kv_read_q4": (_i32, [_KV4P, _RWP, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "bq_kv_read_q8": (_i32, [_KVP, _RWP, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "bq_attn_q4_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "bq_attn_decode_q4": (_i32, [_KV4P, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _i32,
+                                 _vp, _sz, _vp, _vp]),
+}
+
 
 def lib() -> ctypes.CDLL:
     """Load libbq.so; raises if it has not been built (no fallback path)."""
@@ -128,7 +158,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m quantised_weight_gemv_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in {**_SIGS, **_KV_SIGS}.items():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
@@ -138,7 +168,7 @@ def lib() -> ctypes.CDLL:
 
 def __getattr__(name):
     # module-level access to the raw C functions: bq.bq_gemv_q4(...)
-    if name in _SIGS:
+    if name in _SIGS or name in _KV_SIGS:
         return getattr(lib(), name)
     raise AttributeError(name)
 
@@ -304,6 +334,132 @@ def attn_decode_q8(kv: bq_kv_cache, q, lens, G: int, scale: float, o, ws, status
     check("bq_attn_decode_q8", lib().bq_attn_decode_q8(
         ctypes.byref(kv), q.data_ptr(), lens.data_ptr(), B, Hkv, int(G), float(scale), o.data_ptr(),
         ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), _stream_ptr(stream)))
+
+
+def _one_device(fn: str, **tensors) -> None:
+    """Every tensor lies on the current device, whose context the launch uses
+    (the library takes raw pointers and cannot tell)."""
+    import torch
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def kv_cache_q4(k_codes, k_scales, v_codes, v_scales) -> bq_kv_cache_q4:
+    """A bq_kv_cache_q4 over device tensors: codes uint8 [B, Hkv, Tmax, D/2],
+    scales fp16 (bits) [B, Hkv, Tmax, D/32], keys and values alike (the tensors
+    stay owned by the caller; the struct keeps references)."""
+    _on_device("kv_cache_q4", k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales)
+    if k_codes.dim() != 4:
+        raise ValueError("kv_cache_q4: codes must be [B, Hkv, Tmax, D/2]")
+    B, Hkv, Tmax, half = k_codes.shape
+    if (tuple(v_codes.shape) != (B, Hkv, Tmax, half) or half not in (32, 64)
+            or any(tuple(t.shape) != (B, Hkv, Tmax, half // 16) for t in (k_scales, v_scales))
+            or any(not t.is_contiguous() for t in (k_codes, k_scales, v_codes, v_scales))
+            or any(t.element_size() != 1 for t in (k_codes, v_codes))
+            or any(t.element_size() != 2 for t in (k_scales, v_scales))):
+        raise ValueError("kv_cache_q4: shapes/dtypes/contiguity do not match the cache layout")
+    kv = bq_kv_cache_q4(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                        v_scales.data_ptr(), 2 * int(half), int(Tmax))
+    kv._refs = (k_codes, k_scales, v_codes, v_scales)
+    kv.B, kv.Hkv = int(B), int(Hkv)
+    return kv
+
+
+def _dtype_code(fn: str, t) -> int:
+    code = {"torch.float32": BQ_F32, "torch.float16": BQ_F16, "torch.bfloat16": BQ_BF16}.get(str(t.dtype))
+    if code is None:
+        raise ValueError(f"{fn}: dtype {t.dtype} is not float32, float16 or bfloat16")
+    return code
+
+
+def _overlaps(shape, strides) -> bool:
+    """Whether a strided tensor may hold one element twice (extents of 1 aside):
+    each stride must clear everything the smaller ones span."""
+    span = 1
+    for s, n in sorted((s, n) for n, s in zip(shape, strides) if n > 1):
+        if s < span:
+            return True
+        span = s * (n - 1) + span
+    return False
+
+
+def _kv_rows(fn: str, kv, k, v, start, count, status, write: bool) -> bq_kv_rows:
+    """Checks rows k, v ([B, T, Hkv, D] over the cache kv), start and count
+    (int32 [B]); write: the rows are destinations (one of them may be None)."""
+    if not isinstance(kv, (bq_kv_cache, bq_kv_cache_q4)) or not hasattr(kv, "B"):
+        raise ValueError(f"{fn}: kv must come from kv_cache or kv_cache_q4")
+    given = [t for t in (k, v) if t is not None]
+    if len(given) < (1 if write else 2):
+        raise ValueError(f"{fn}: " + ("k or v must be given" if write else "k and v must be given"))
+    _on_device(fn, k=k, v=v, start=start, count=count, status=status)
+    T = given[0].shape[1] if given[0].dim() == 4 else -1
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            continue
+        if tuple(t.shape) != (kv.B, T, kv.Hkv, kv.D) or T < 1 or t.stride(3) != 1:
+            raise ValueError(f"{fn}: {name} must be [{kv.B}, T, {kv.Hkv}, {kv.D}] with contiguous rows, got "
+                             f"{tuple(t.shape)}")
+        if t.dtype != given[0].dtype:
+            raise ValueError(f"{fn}: k and v must have one dtype")
+        if write and _overlaps(t.shape, t.stride()):
+            raise ValueError(f"{fn}: {name}'s rows overlap")
+    for name, t in (("start", start), ("count", count)):
+        if t is not None and (t.numel() != kv.B or str(t.dtype) != "torch.int32" or not t.is_contiguous()):
+            raise ValueError(f"{fn}: {name} must be int32 [{kv.B}]")
+    dt = _dtype_code(fn, given[0])
+
+    def strides(t):                  # a stride over an extent of 1 is never used
+        return [0, 0, 0] if t is None else [s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])]
+    _one_device(fn, cache=kv._refs[0], k=k, v=v, start=start, count=count, status=status)
+    return bq_kv_rows(_ptr(k), _ptr(v), *strides(k), *strides(v), dt, int(T))
+
+
+def kv_append(kv, k, v, start, count=None, status=None, stream=None) -> None:
+    """Quantise rows k, v ([B, T, Hkv, D], fp32 / fp16 / bf16, any strides with
+    contiguous rows) into positions start[b] .. start[b] + count[b] - 1 of the
+    cache (count None: T rows each), through bq_kv_append_q4 or _q8 as kv is a
+    Q4 or a Q8 cache.  start and count are int32 [B] on the device."""
+    rows = _kv_rows("kv_append", kv, k, v, start, count, status, False)
+    name = "bq_kv_append_q4" if isinstance(kv, bq_kv_cache_q4) else "bq_kv_append_q8"
+    check(name, getattr(lib(), name)(ctypes.byref(kv), ctypes.byref(rows), kv.B, kv.Hkv, start.data_ptr(),
+                                     _ptr(count), _ptr(status), _stream_ptr(stream)))
+
+
+def kv_read(kv, k, v, start, count=None, status=None, stream=None) -> None:
+    """Read positions start[b] .. start[b] + count[b] - 1 of the cache into rows
+    k, v ([B, T, Hkv, D], fp32 / fp16 / bf16; either may be None) through
+    bq_kv_read_q4 or _q8.  Rows from count[b] on are left as they were."""
+    rows = _kv_rows("kv_read", kv, k, v, start, count, status, True)
+    name = "bq_kv_read_q4" if isinstance(kv, bq_kv_cache_q4) else "bq_kv_read_q8"
+    check(name, getattr(lib(), name)(ctypes.byref(kv), ctypes.byref(rows), kv.B, kv.Hkv, start.data_ptr(),
+                                     _ptr(count), _ptr(status), _stream_ptr(stream)))
+
+
+def attn_decode_q4(kv: bq_kv_cache_q4, q, lens, G: int, scale: float, o, ws, status=None,
+                   stream=None) -> None:
+    """o = softmax(scale q K^T) V over the Q4 cache (bq_attn_decode_q4).  q and
+    o are [B, Hkv*G, D] (one query token a sequence) or [B, Tq, Hkv*G, D]; q
+    fp16 bits, o fp32 or fp16.  Query token i of sequence b attends to the
+    positions below lens[b] - (Tq - 1 - i)."""
+    if not isinstance(kv, bq_kv_cache_q4) or not hasattr(kv, "B"):
+        raise ValueError("attn_decode_q4: kv must come from kv_cache_q4")
+    _on_device("attn_decode_q4", q=q, lens=lens, o=o, ws=ws, status=status)
+    B, Hkv = kv.B, kv.Hkv
+    Tq = q.shape[1] if q.dim() == 4 else 1
+    want = (B, Tq, Hkv * G, kv.D) if q.dim() == 4 else (B, Hkv * G, kv.D)
+    if tuple(q.shape) != want or q.element_size() != 2 or "bfloat16" in str(q.dtype) or not q.is_contiguous():
+        raise ValueError(f"attn_decode_q4: q must be contiguous fp16 bits [{B}, (Tq,) {Hkv * G}, {kv.D}]")
+    if lens.numel() != B or str(lens.dtype) != "torch.int32" or not lens.is_contiguous():
+        raise ValueError(f"attn_decode_q4: lens must be int32 [{B}]")
+    od = _dtype_code("attn_decode_q4", o)
+    if tuple(o.shape) != want or od == BQ_BF16 or not o.is_contiguous():
+        raise ValueError(f"attn_decode_q4: o must be contiguous float32 or float16 of q's shape {want}")
+    _one_device("attn_decode_q4", cache=kv._refs[0], q=q, lens=lens, o=o, ws=ws, status=status)
+    check("bq_attn_decode_q4", lib().bq_attn_decode_q4(
+        ctypes.byref(kv), q.data_ptr(), lens.data_ptr(), B, int(Tq), Hkv, int(G), float(scale), o.data_ptr(),
+        od, ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), _stream_ptr(stream)))
 
 
 def moe_gemv_q4(Wstack: bq_qmat, E: int, codes_stride: int, scales_stride: int, x,

@@ -34,7 +34,7 @@ def nvcc() -> str:
 
 def _deps() -> list:
     return (glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
-            [os.path.join(INCLUDE, "bq.h"), os.path.abspath(__file__)])
+            [os.path.join(INCLUDE, "bq.h"), os.path.join(INCLUDE, "bq_kv.h"), os.path.abspath(__file__)])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "bq_internal.h"
+#include "bq_kv.h"
 
 namespace bq {
 
@@ -115,6 +116,7 @@ extern "C" const char *bq_status_string(int32_t s)
     case BQ_ERR_TIMEOUT: return "bounded wait timed out";
     case BQ_ERR_WORKSPACE: return "workspace missing or too small";
     case BQ_ERR_RANGE: return "value out of range";
+    case BQ_ERR_POSITION: return "cache position or row count out of range";
     default: return "unknown status";
     }
 }
