@@ -37,18 +37,26 @@ def random_cache_q4(seed, B, Hkv, Tmax, D, k_size=1.0, v_size=1.0):
 
 
 def attention_ref(planes, q_bits, lens, G, scale):
-    """(o, sum_t p_t |V|, slack) in fp64 for q_bits [B, Tq, Hkv*G, D].
+    """(o, sum_t p_t |V|, slack, floor) in fp64 for q_bits [B, Tq, Hkv*G, D].
 
     slack[b, i, j] bounds the relative error that fp32 scores bring into a
     softmax weight.  A score is sum over blocks of dK * (sum_d u q - 8 sum_d q)
     with codes u <= 15: its terms add up to at most S = scale * sum_d |q_d|
     23 dK, each accumulation step keeps them to 2^-23 of that, and a block takes
     three steps (four with the sum over blocks); exp doubles it (numerator and
-    sum).  The exponent's argument adds 2^-23 of its own magnitude."""
+    sum).  The exponent's argument adds 2^-23 of its own magnitude.
+
+    floor[b, i, j] is absolute: a weight p_t dV enters the value product as
+    2^(s_t - m) dV in fp16, whose spacing is 2^-24 below 2^-14, so each of n
+    positions may be off by 2^-25 times a code of at most 8.  The reference m is
+    at most max_t s_t + E - 11 with 2^E <= 1.07 max(dV, 2^-14), and the sum of
+    2^(s_t) is at least 2^(max s_t): off by at most n 8 2^-25 2^(E - 11) <=
+    n 2^-32 max(dV, 2^-14) in o.  It shows where the leading positions' codes
+    are 0 and o consists of positions with weights below 2^-20."""
     kc, ks, vc, vs = planes
     q = q_bits.view(np.float16).astype(np.float64)
     B, Tq, H, D = q.shape
-    o, ao, slack = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:3])
+    o, ao, slack, floor = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:3]), np.zeros(q.shape[:3])
     for b in range(B):
         n = min(max(int(lens[b]), 0), kc.shape[2])
         if n == 0:
@@ -65,20 +73,21 @@ def attention_ref(planes, q_bits, lens, G, scale):
                     p = np.exp(s - s.max())
                     p /= p.sum()
                     o[b, i, j], ao[b, i, j] = p @ V[:m], p @ np.abs(V[:m])
+                    floor[b, i, j] = m * 2.0 ** -32 * max(oracle.half_to_double(vs[b, h, :m]).max(), 2.0 ** -14)
                     S = abs(scale) * 23 * (dk[:m] @ np.abs(q[b, i, j]).reshape(-1, 32).sum(-1)).max()
                     slack[b, i, j] = 2 * 4 * 2.0 ** -23 * S + 2.0 ** -22 * 1.4427 * np.abs(s).max()
-    return o, ao, slack
+    return o, ao, slack, floor
 
 
 def check_attention(o, ref, f16):
-    """|o - o_ref| <= A (r + slack + 2^-16) + |o_ref| 2^-11 + 2^-24, A = sum p |V|:
+    """|o - o_ref| <= A (r + slack + 2^-16) + floor + |o_ref| 2^-11 + 2^-24, A = sum p |V|:
     r = 2^-11 is a softmax weight's one rounding to fp16 when the output is
     fp16 (two fp16 terms otherwise: below 2^-20), 2^-16 = 128 fp32 roundings of
     sums of signed terms, and the last two are the fp16 output's rounding."""
-    o_ref, ao, slack = ref
+    o_ref, ao, slack, floor = ref
     o = np.asarray(o, dtype=np.float64)
     assert o.shape == o_ref.shape and np.all(np.isfinite(o))
-    bound = ao * ((2.0 ** -11 if f16 else 2.0 ** -20) + 2.0 ** -16 + slack[..., None])
+    bound = ao * ((2.0 ** -11 if f16 else 2.0 ** -20) + 2.0 ** -16 + slack[..., None]) + floor[..., None]
     bound += (2.0 ** -11 * np.abs(o_ref) + 2.0 ** -24) if f16 else 2.0 ** -126
     bad = np.argwhere(np.abs(o - o_ref) > bound)
     assert bad.size == 0, (len(bad), bad[:4].tolist(), float(np.max(np.abs(o - o_ref) / bound)))
