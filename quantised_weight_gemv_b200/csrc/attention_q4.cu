@@ -7,13 +7,14 @@
 // what stands against it is the number of instructions that unpack 256 codes.
 //
 // Work: a unit is 32 positions of one (sequence, KV head).  The valid units of
-// all sequences form one line (lens are on the device, so every CTA builds the
+// all sequences form one line (lens are on the device, so every warp builds the
 // prefix sums itself); CTAs take equal consecutive shares of it, and a CTA's
 // workers (warps) equal consecutive shares of the CTA's.  Ragged lengths
 // therefore cost no balance, and a sequence that ends inside a share just
 // starts the next one: a warp never waits for another before its line ends.
-// A warp streams its units through a ring of its own in shared memory (TMA,
-// refilled by the warp itself, so a slot needs no "empty" barrier).
+// A warp streams its units through a ring of its own in shared memory with
+// 16-byte cp.async, laid down in a swizzle that keeps ldmatrix free of bank
+// conflicts; no barrier, and nothing that could wait for ever.
 //
 // Softmax: one pass with a running reference m a row; a warp's result of a
 // segment (the part of a sequence's head in its share) is (m, l, O).  A whole
@@ -23,19 +24,20 @@
 //
 // Tensor cores (mma.sync m16n8k16; with 8 or 16 rows a tcgen05 tile of 128
 // rows would be empty), fp32 accumulation, codes exact:
-//   scores  S[row][t]: A = q, B = key codes u (0..15) as fp16 subnormals
-//     u 2^-24 (the masked nibble is the whole conversion; the high nibble is
-//     16 u, so q enters times 1/16 there).  The zero point is the accumulator's
-//     start, -8 2^-24 sum(q) a block.  Each block is scaled by dK in fp32.  q is
-//     multiplied by a power of two a row first so that both forms are exact.
+//   scores  S^T[t][row]: A = key codes u (0..15) as fp16 subnormals u 2^-24 (the
+//     masked nibble is the whole conversion; the high nibble is 16 u, so q
+//     enters times 1/16 there), B = q.  Positions fill the 16-row side, so no
+//     operand is padded.  Each block's sum, less its zero point
+//     8 2^-24 sum(q), is scaled by dK in fp32.  q is multiplied by a power of two
+//     a row first so that both forms are exact.
 //   values  O^T[d][row]: A = value codes u - 8 (exact fp16: (0x6400 | u) - 1032),
 //     signed so that sums over thousands of positions do not cancel against a
 //     zero-point sum, B = p dV rounded to fp16.  ldmatrix.trans on 16-bit units
 //     turns position-major rows into pairs of positions per register.
-//   The score accumulators have the layout B needs: p stays in registers.
+//   p dV reaches B's layout by one movmatrix a tile and never leaves registers.
 // Scaling of p: fp16 must neither overflow nor go subnormal where it counts, so
-// a row's reference bounds p dV instead of p: m = max(s + log2 dV) - 11, with
-// log2 of a lane's largest value scale taken as bits / 1024 - 15 (at most 0.09
+// a row's reference bounds p dV instead of p: m = max s + log2 dV - 11, with
+// log2 of a unit's largest value scale taken as bits / 1024 - 15 (at most 0.09
 // low, up to 9 high for subnormals).  O and l carry the same 2^-m.  m moves
 // only when the bound outgrows it by 2^4: p dV < 2^15.1.
 #include <cuda_fp16.h>
@@ -56,7 +58,6 @@ constexpr int kMaxGrid = 256;             // CTAs (one per SM)
 constexpr int kPassRows = 64;             // query rows per pass over a segment (NT = 2)
 constexpr float kFloor = -3.0e38f;        // a reference no score has reached
 constexpr float kBase = 11.0f, kSlack = 4.0f;
-constexpr int kScan = 256;                // chunks of the prefix sums
 
 // D: head width; NT: 8-row tiles per warp (1: R <= 8; 2: 16 rows).
 template <int D, int NT>
@@ -69,17 +70,17 @@ struct Cfg {
     static constexpr int kCodes = kUnit * D / 2, kScales = kUnit * kNB * 2;
     static constexpr int kSlotBytes = 2 * (kCodes + kScales);
     static constexpr int kRing = kSlots * kSlotBytes;         // per warp
-    static constexpr int kLd = D + 8;                         // floats per row of a partial in shared memory
+    static constexpr int kLd = D;                             // floats per row of a partial in shared memory
+    static constexpr int kConv = 2 * kUnit * kNB * 4;         // a unit's scales in fp32 (keys, values)
     static constexpr int kPart = kRows * kLd + 2 * kRows;     // floats: O, m, l
-    static constexpr size_t kSmem = 1024 + (size_t)kWarps * (kRing + kPart * 4);
+    static constexpr size_t kSmem = 128 + (size_t)kWarps * (kRing + kPart * 4 + kConv);
     static_assert(kPart * 4 <= kRing, "a warp's last partial fits its drained ring");
-    static_assert(kSlotBytes % 512 == 0 || D == 64, "slots keep the swizzle's period");
-    static_assert(kSlotBytes % 256 == 0, "slots keep the swizzle's period");
-    static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
+    static_assert(kSlotBytes % 128 == 0 && kPart % 4 == 0, "slots and partials keep their alignment");
+    static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of an SM");
 };
 
 struct Args {
-    CUtensorMap tm_k, tm_v;               // (D/2 bytes, B*Hkv*Tmax rows), box 32 rows, swizzled
+    const uint8_t *kc, *vc;
     const uint16_t *ks, *vs, *q;
     const int32_t *lens;
     void *o;
@@ -88,12 +89,11 @@ struct Args {
     int rg, passes;                       // 16-row groups per CTA (1, 2, 4), passes of 16 rg rows
     float scale2;                         // scale * log2(e)
     int *counters;                        // [grid], by a shared segment's first CTA
-    float *partials;                      // [grid][2][rows][D + 2]
-    int *status;
+    float *partials;                      // [grid][2]: O [rows][D], then (m, l) [rows]
 };
 
 struct Entry {                            // a shared segment's part, for the merges
-    int b, hp, first, units;              // sequence, head * passes + pass, first unit on the line, units
+    int b, hp, first, units;              // sequence (-1: none), head * passes + pass, first unit on the line, units
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -117,6 +117,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -127,22 +133,50 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// The scale words of two consecutive positions: w[position][block pair].
+// A position's fp32 scales.
 template <int NB>
-__device__ __forceinline__ void scale_words(uint32_t (&w)[2][NB / 2], uint32_t addr)
+__device__ __forceinline__ void row_scales(float (&d)[NB], uint32_t addr)
 {
     if constexpr (NB == 4)
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0][0]), "=r"(w[0][1]), "=r"(w[1][0]), "=r"(w[1][1]) : "r"(addr) : "memory");
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(addr) : "memory");
     else
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0][0]), "=r"(w[1][0]) : "r"(addr) : "memory");
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(d[0]), "=f"(d[1]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy)
+// One position's fp16 scales to fp32, shared to shared memory (mask: 0 or ~0);
+// returns the bits of the largest.
+template <int NB>
+__device__ __forceinline__ uint32_t convert_scales(uint32_t dst, uint32_t src, bool live)
 {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
+    uint32_t w[NB / 2];
+    if constexpr (NB == 4)
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(src) : "memory");
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < NB / 2; i++) {
+        w[i] = live ? w[i] : 0u;
+        mx = __vmaxu2(mx, w[i]);
+    }
+    if constexpr (NB == 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "f"(f16_lo(w[0])), "f"(f16_hi(w[0])), "f"(f16_lo(w[1])), "f"(f16_hi(w[1])) : "memory");
+    else
+        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(dst), "f"(f16_lo(w[0])), "f"(f16_hi(w[0])) : "memory");
+    return max(mx & 0x7fffu, (mx >> 16) & 0x7fffu);
 }
-// Byte offset of 16-byte chunk `chunk` of a row as TMA's 64- or 32-byte swizzle lays it down.
+// 16 bytes to shared memory, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x)      // an 8 x 8 tile of 16-bit elements over the warp
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// Byte offset of 16-byte chunk `chunk` (block) of position `row` in a unit: the
+// chunks of 8 consecutive positions fall into all 32 banks.
 template <int D>
 __device__ __forceinline__ uint32_t swizzled(int row, int chunk)
 {
@@ -164,8 +198,16 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t x)
     return h;
 }
 
-// The CTA (or worker) owning unit x when n of them share U units.
-__device__ __forceinline__ int owner_of(long long x, int U, int n) { return (int)(((x + 1) * n - 1) / U); }
+// Units shared by CTAs: q each, one more for the first r.
+struct Shares {
+    int q, r;
+    __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
+    __device__ __forceinline__ int owner(int x) const
+    {
+        const int big = r * (q + 1);
+        return x < big ? x / (q + 1) : r + (x - big) / q;
+    }
+};
 
 template <typename O>
 __device__ __forceinline__ void store2(O *p, float a, float b)
@@ -174,6 +216,15 @@ __device__ __forceinline__ void store2(O *p, float a, float b)
         *reinterpret_cast<float2 *>(p) = make_float2(a, b);
     else
         *reinterpret_cast<uint32_t *>(p) = pack_f16x2(a, b);
+}
+
+template <typename O>
+__device__ __forceinline__ void store4(O *p, const float4 &v, float f)
+{
+    if constexpr (sizeof(O) == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    else
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_f16x2(v.x * f, v.y * f), pack_f16x2(v.z * f, v.w * f));
 }
 
 // A place on the line of units: unit t of nu of (sequence b, head-pass hp).
@@ -188,41 +239,35 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     constexpr int NB = C::kNB, W = C::kWarps, S = C::kSlots;
     constexpr bool kTwo = sizeof(O) == 4;             // p dV as two fp16 terms
     extern __shared__ uint8_t smem_raw[];
-    __shared__ alignas(8) uint64_t bar_full[W][S];
-    __shared__ int pre[kScan + 1];
-    __shared__ Entry entry[W][2];
-    __shared__ int scan_tmp[kScan / 32];
+    __shared__ Entry entry[2 * W];                    // worker w: 2w (began before its share), 2w + 1
     __shared__ int arrived[2];
 
-    uint8_t *sbase = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sbase = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t ring = smem_u32(sbase) + warp * C::kRing;
     float *first_part = reinterpret_cast<float *>(sbase + W * C::kRing) + warp * C::kPart;
     float *last_part = reinterpret_cast<float *>(sbase + warp * C::kRing);
+    const uint32_t conv = smem_u32(sbase) + W * (C::kRing + C::kPart * 4) + warp * C::kConv;
     const int HP = a.Hkv * a.passes;
 
-    if (lane == 0) {
-        for (int i = 0; i < S; i++)
-            mbar_init(smem_u32(&bar_full[warp][i]), 1);
-        fence_barrier_init();
-        prefetch_tensormap(&a.tm_k);
-        prefetch_tensormap(&a.tm_v);
-    }
     if (threadIdx.x < W * 2)
-        entry[threadIdx.x >> 1][threadIdx.x & 1].b = -1;
+        entry[threadIdx.x].b = -1;
     pdl_launch_dependents();
     pdl_wait();
 
     auto length = [&](int b) { return min(max(a.lens[b], 0), a.Tmax); };
     auto units_of = [&](int b) { return (length(b) + kUnit - 1) / kUnit; };
 
-    // -------- prefix sums of the units per sequence (of one head and pass) ----
-    const int chunk = (a.B + kScan - 1) / kScan;
+    // -------- prefix sums of the units per sequence (of one head and pass):
+    // lane i holds the sum before its chunk of sequences ----
+    const int chunk = (a.B + 31) / 32;
+    int before_chunk, U;
     {
         int sum = 0;
-        if (threadIdx.x < kScan)
-            for (int b = threadIdx.x * chunk; b < min(a.B, ((int)threadIdx.x + 1) * chunk); b++)
-                sum += units_of(b);
+        const int b1 = min(a.B, (lane + 1) * chunk);
+#pragma unroll 4
+        for (int b = lane * chunk; b < b1; b++)
+            sum += units_of(b);
         int inc = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -230,22 +275,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             if (lane >= off)
                 inc += v;
         }
-        if (threadIdx.x < kScan && lane == 31)
-            scan_tmp[warp] = inc;
-        __syncthreads();
-        if (threadIdx.x < kScan) {
-            int base = 0;
-            for (int w = 0; w < warp; w++)
-                base += scan_tmp[w];
-            pre[threadIdx.x + 1] = base + inc;
-            if (threadIdx.x == 0)
-                pre[0] = 0;
-        }
-        __syncthreads();
+        before_chunk = inc - sum;
+        U = __shfl_sync(0xffffffffu, inc, 31) * HP;
     }
-    const int U = pre[kScan] * HP;
-    const int NW = W / a.rg;                          // workers; a worker is rg warps, one per row group
-    const int n_act = min((int)gridDim.x, (U + NW - 1) / NW);
+    // workers; a worker is rg (1, 2, 4) warps, one per row group
+    const int rg_log = a.rg >> 1, nw_log = (W == 16 ? 4 : 3) - rg_log, NW = 1 << nw_log;
+    const int n_act = min((int)gridDim.x, (U + NW - 1) >> nw_log);
     const int cta = blockIdx.x;
 
     // -------- sequences without positions ----
@@ -258,9 +293,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         }
     if (cta >= n_act)
         return;
-    const int r0 = (int)((long long)cta * U / n_act), r1 = (int)((long long)(cta + 1) * U / n_act);
-    const int wk = warp / a.rg, rgi = warp % a.rg;
-    const int w0 = r0 + (int)((long long)wk * (r1 - r0) / NW), w1 = r0 + (int)((long long)(wk + 1) * (r1 - r0) / NW);
+    const Shares sh = {U / n_act, U % n_act};
+    const int r0 = sh.start(cta), r1 = sh.start(cta + 1);
+    const int wk = warp >> rg_log, rgi = warp & (a.rg - 1);
+    // (workers without units, if any, are the CTA's last: the merge counts on it)
+    const Shares ws = {(r1 - r0) >> nw_log, (r1 - r0) & (NW - 1)};
+    const int w0 = r0 + ws.start(wk), w1 = r0 + ws.start(wk + 1);
 
     auto next_seq = [&](Cursor &c) {                  // the next sequence with units
         c.hp = 0;
@@ -269,21 +307,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             c.nu = c.b < a.B ? units_of(c.b) : 1;
         } while (c.nu == 0);
     };
-    auto advance = [&](Cursor &c) {
-        if (++c.t == c.nu) {
-            c.t = 0;
-            if (++c.hp == HP)
-                next_seq(c);
-        }
-    };
     Cursor cur = {0, 0, 0, 1};
     if (w0 < w1) {
-        // the chunk holding unit w0: the last with pre * HP <= w0
-        const unsigned m1 = __ballot_sync(0xffffffffu, (long long)pre[8 * lane] * HP <= w0);
-        const int c8 = (31 - __clz(m1)) * 8;
-        const unsigned m2 = __ballot_sync(0xffffffffu, lane < 8 && (long long)pre[c8 + (lane & 7)] * HP <= w0);
-        const int ci = c8 + 31 - __clz(m2);
-        int left = w0 - pre[ci] * HP;
+        // the chunk holding unit w0: the last that begins at or before it
+        const unsigned m1 = __ballot_sync(0xffffffffu, lane * chunk < a.B && before_chunk * HP <= w0);
+        const int ci = 31 - __clz(m1);
+        int left = w0 - __shfl_sync(0xffffffffu, before_chunk, ci) * HP;
         cur.b = ci * chunk - 1;
         for (next_seq(cur); left >= cur.nu * HP; next_seq(cur))
             left -= cur.nu * HP;
@@ -292,53 +321,66 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     }
 
     // ------------------------------------------------------- the ring ----
-    const bool stream_once = a.passes == 1 && a.rg == 1;
-    const uint64_t pol = stream_once ? policy_evict_first() : policy_evict_normal();
-    Cursor is = cur;
-    int issued = 0;
     // row groups past the last row have nothing to do
     auto idle_pass = [&](int hp) { return NT == 2 && (hp % a.passes) * kPassRows + rgi * 16 >= a.R; };
-    auto issue = [&]() {                              // lane 0
-        const int slot = issued % S;
-        const uint32_t bar = smem_u32(&bar_full[warp][slot]), base = ring + slot * C::kSlotBytes;
-        const size_t row = ((size_t)is.b * a.Hkv + is.hp / a.passes) * a.Tmax + is.t * kUnit;
-        mbar_arrive_expect_tx(bar, C::kSlotBytes);
-        tma_load_2d(base, &a.tm_k, bar, 0, (int)row, pol);
-        tma_load_2d(base + C::kCodes, &a.tm_v, bar, 0, (int)row, pol);
-        bulk_load(base + 2 * C::kCodes, a.ks + row * NB, C::kScales, bar, pol);
-        bulk_load(base + 2 * C::kCodes + C::kScales, a.vs + row * NB, C::kScales, bar, pol);
+    // lane i copies chunk i % NB of positions i / NB, + 32 / NB, ... of keys and
+    // values, then 16 bytes of the scales (one half-warp each)
+    constexpr int kPer = 32 / NB;                     // positions per step: a multiple of the swizzle's period
+    constexpr int kSc = C::kScales / 16;              // lanes per scale plane: 16 or 8
+    const uint32_t lane_dst = swizzled<D>(lane / NB, lane % NB);
+    // what is copied next: position row `is_row` of the planes, `is_left` units of its segment, `to_issue` in all
+    Cursor is = cur;
+    int is_left = cur.nu - cur.t, to_issue = w1 - w0;
+    auto seg_row = [&](const Cursor &c) { return (c.b * a.Hkv + (a.passes == 1 ? c.hp : c.hp / a.passes)) * a.Tmax; };
+    int is_row = seg_row(cur) + cur.t * kUnit;
+    auto issue = [&](uint32_t base) {
+        if (to_issue > 0) {
+            const size_t off = (size_t)(unsigned)is_row * (D / 2) + lane * 16;
+            const uint8_t *kp = a.kc + off, *vp = a.vc + off;
+#pragma unroll
+            for (int i = 0; i < kUnit / kPer; i++) {
+                copy16(base + lane_dst + i * 512, kp + i * 512);
+                copy16(base + lane_dst + C::kCodes + i * 512, vp + i * 512);
+            }
+            if (lane < 2 * kSc)
+                copy16(base + 2 * C::kCodes + lane * 16,
+                       (lane < kSc ? a.ks : a.vs) + (size_t)(unsigned)is_row * NB + (lane & (kSc - 1)) * 8);
+            to_issue--;
+            is_row += kUnit;
+            if (--is_left == 0) {
+                if (++is.hp == HP)
+                    next_seq(is);
+                is_left = is.nu;
+                is_row = seg_row(is);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const int total = w1 - w0;
-    for (int k = 0; k < S && issued < total; k++) {
-        if (lane == 0)
-            issue();
-        issued++;
-        advance(is);
-    }
+#pragma unroll
+    for (int k = 0; k < S; k++)
+        issue(ring + k * C::kSlotBytes);
 
     // ------------------------------------------------------ the stream ----
-    bool ok = true;
-    int n = 0;                                        // units consumed
+    uint32_t kb = ring;                               // slot of the unit at hand
     int u = w0;
-    bool any_first = false, any_last = false;
-    Entry ent_first, ent_last;
-    while (u < w1 && ok) {
+    while (u < w1) {
         const int sb = cur.b, shp = cur.hp, st0 = cur.t, snu = cur.nu;
         const int ue = min(w1, u + snu - st0);
         const int h = shp / a.passes, row_base = (shp % a.passes) * kPassRows + rgi * 16;
         const int L = length(sb);
         const bool idle = idle_pass(shp);
 
-        // query fragments: block j, half hf (low / high nibbles); rows g (and g + 8)
+        // query fragments (B of the score product): block j, half hf (low / high
+        // nibbles); the lane's row is g of each tile.  What follows a score is
+        // held for the accumulator's rows, 2 t4 + e.
         uint32_t qf[NT][NB][2][2];
-        float mul[NT], koff[NT][NB];
-        int lim[NT];                                  // positions row sees
+        float mul[NT][2], koff[NT][NB][2];
+        int lim[NT][2];                               // positions a row sees
 #pragma unroll
         for (int r = 0; r < NT; r++) {
             const int row = row_base + g + 8 * r;
             const bool live = row < a.R;
             const int tok = live ? row / a.G : 0;
-            lim[r] = L - (a.Tq - 1 - tok);
             const uint16_t *qp = a.q + (((size_t)sb * a.Tq + tok) * a.Hkv * a.G + (size_t)h * a.G + (live ? row % a.G : 0)) * D;
             uint2 v[NB][2];
             uint32_t mx = 0;
@@ -354,8 +396,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             const int top = (int)max(mx & 0xffffu, mx >> 16);
             // max |q| 2^k in [2^13, 2^14) (exact for subnormal rows too); inf and NaN pass through
             const int k = top == 0 || top >= 0x7c00 ? 0 : 28 - max(top >> 10, 1);
-            const float f = pow2i(k);
-            mul[r] = a.scale2 * pow2i(24 - k);
+            const float f = a.scale2 < 0.0f ? -pow2i(k) : pow2i(k);
+            // positive, so that a masked score of -inf stays one
+            const float back = fmaxf(fabsf(a.scale2) * pow2i(24 - k), 1e-37f);
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                mul[r][e] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4 * e);
+                lim[r][e] = L - (a.Tq - 1 - __shfl_sync(0xffffffffu, tok, 8 * t4 + 4 * e));
+            }
 #pragma unroll
             for (int j = 0; j < NB; j++) {
                 float z[4] = {0.f, 0.f, 0.f, 0.f};
@@ -367,142 +415,143 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                     qf[r][j][hf][1] = pack_f16x2(f16_hi(v[j][hf].x) * fh, f16_hi(v[j][hf].y) * fh);
                     // -8 2^-24 (-128 2^-24) as fp16 subnormals
                     const uint32_t zp = hf ? 0x80808080u : 0x80088008u;
-                    mma(z, qf[r][j][hf][0], 0u, qf[r][j][hf][1], 0u, zp, zp);
+                    mma(z, zp, zp, zp, zp, qf[r][j][hf][0], qf[r][j][hf][1]);
                 }
-                koff[r][j] = z[0];
+                koff[r][j][0] = z[0];
+                koff[r][j][1] = z[1];
             }
         }
-        float m[NT], l[NT], acc[NT][2 * NB][4];
+        float m[NT][2], l[NT][2], acc[NT][2 * NB][4];
 #pragma unroll
         for (int r = 0; r < NT; r++) {
-            m[r] = kFloor;
-            l[r] = 0.0f;
+            m[r][0] = m[r][1] = kFloor;
+            l[r][0] = l[r][1] = 0.0f;
 #pragma unroll
             for (int i = 0; i < 2 * NB; i++)
                 acc[r][i][0] = acc[r][i][1] = acc[r][i][2] = acc[r][i][3] = 0.0f;
         }
 
-        for (; u < ue; u++, n++) {
-            const int slot = n % S;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_full[warp][slot]), (n / S) & 1));
-            if (!ok)
-                break;
-            const uint32_t kb = ring + slot * C::kSlotBytes, vb = kb + C::kCodes;
-            const uint32_t ksb = kb + 2 * C::kCodes, vsb = ksb + C::kScales;
-            const int t0 = cur.t * kUnit;
+        int t0 = st0 * kUnit;
+        for (; u < ue; u++, t0 += kUnit) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+            __syncwarp();                             // every lane's copies of this unit have landed
+            const uint32_t vb = kb + C::kCodes;
             if (!idle) {
+                // ------------------------------------------ scales ----
+                // lane i converts position i's; past the length the cache may
+                // hold anything: scales of 0
+                const bool valid = t0 + lane < L;
+                (void)convert_scales<NB>(conv + lane * NB * 4, kb + 2 * C::kCodes + lane * NB * 2, valid);
+                const uint32_t vmax = __reduce_max_sync(
+                    0xffffffffu, convert_scales<NB>(conv + (kUnit + lane) * NB * 4, kb + 2 * C::kCodes + C::kScales + lane * NB * 2, valid));
+                __syncwarp();
                 // ------------------------------------------ scores ----
+                // s[r][p][e]: row 2 t4 + e of tile r, position 8 p + g
                 float s[NT][4][2];
 #pragma unroll
-                for (int nt = 0; nt < 4; nt++) {
-                    uint32_t kx[NB];
+                for (int mt = 0; mt < 2; mt++) {      // 16 positions
+                    uint32_t kx[2][NB];
                     if constexpr (D == 128) {
-                        ldsm4(kx, kb + swizzled<D>(8 * nt + (lane & 7), lane >> 3));
-                    } else {
-                        uint32_t two[4];              // n-tiles nt & ~1 and | 1, blocks 0 and 1
-                        ldsm4(two, kb + swizzled<D>(8 * ((nt & ~1) + (lane >> 4)) + (lane & 7), (lane >> 3) & 1));
-                        kx[0] = two[2 * (nt & 1)];
-                        kx[1] = two[2 * (nt & 1) + 1];
-                    }
-                    uint32_t w[2][NB / 2];
-                    scale_words<NB>(w, ksb + (8 * nt + 2 * t4) * NB * 2);
 #pragma unroll
-                    for (int r = 0; r < NT; r++)
-                        s[r][nt][0] = s[r][nt][1] = 0.0f;
+                        for (int i = 0; i < 2; i++)
+                            ldsm4(kx[i], kb + swizzled<D>(16 * mt + 8 * i + (lane & 7), lane >> 3));
+                    } else {
+                        uint32_t t[4];                // positions 0-7: blocks 0, 1; positions 8-15: blocks 0, 1
+                        ldsm4(t, kb + swizzled<D>(16 * mt + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
+                        kx[0][0] = t[0], kx[0][1] = t[1], kx[1][0] = t[2], kx[1][1] = t[3];
+                    }
+                    float dk[2][NB];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        row_scales<NB>(dk[i], conv + (16 * mt + 8 * i + g) * NB * 4);
+#pragma unroll
+                        for (int r = 0; r < NT; r++)
+#pragma unroll
+                            for (int e = 0; e < 2; e++) {
+                                float z = dk[i][0] * koff[r][0][e];
+#pragma unroll
+                                for (int j = 1; j < NB; j++)
+                                    z = fmaf(dk[i][j], koff[r][j][e], z);
+                                s[r][2 * mt + i][e] = z;
+                            }
+                    }
 #pragma unroll
                     for (int j = 0; j < NB; j++) {
-                        float c[4];
-                        c[0] = c[1] = koff[0][j];
-                        c[2] = c[3] = NT == 2 ? koff[NT - 1][j] : 0.0f;
-                        const uint32_t x = kx[j], y = x >> 8;
-                        mma(c, qf[0][j][0][0], NT == 2 ? qf[NT - 1][j][0][0] : 0u, qf[0][j][0][1],
-                            NT == 2 ? qf[NT - 1][j][0][1] : 0u, x & 0x000F000Fu, y & 0x000F000Fu);
-                        mma(c, qf[0][j][1][0], NT == 2 ? qf[NT - 1][j][1][0] : 0u, qf[0][j][1][1],
-                            NT == 2 ? qf[NT - 1][j][1][1] : 0u, x & 0x00F000F0u, y & 0x00F000F0u);
-                        const float d0 = j & 1 ? f16_hi(w[0][j >> 1]) : f16_lo(w[0][j >> 1]);
-                        const float d1 = j & 1 ? f16_hi(w[1][j >> 1]) : f16_lo(w[1][j >> 1]);
+                        const uint32_t x0 = kx[0][j], x1 = kx[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
+                        float c[NT][4];
 #pragma unroll
-                        for (int r = 0; r < NT; r++) {
-                            s[r][nt][0] = fmaf(d0, c[2 * r], s[r][nt][0]);
-                            s[r][nt][1] = fmaf(d1, c[2 * r + 1], s[r][nt][1]);
-                        }
-                    }
+                        for (int r = 0; r < NT; r++)
+                            mma0(c[r], x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu,
+                                 qf[r][j][0][0], qf[r][j][0][1]);
 #pragma unroll
-                    for (int r = 0; r < NT; r++) {
-                        s[r][nt][0] *= mul[r];
-                        s[r][nt][1] *= mul[r];
+                        for (int r = 0; r < NT; r++)
+                            mma(c[r], x0 & 0x00F000F0u, x1 & 0x00F000F0u, y0 & 0x00F000F0u, y1 & 0x00F000F0u,
+                                qf[r][j][1][0], qf[r][j][1][1]);
+#pragma unroll
+                        for (int r = 0; r < NT; r++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++)
+#pragma unroll
+                                for (int e = 0; e < 2; e++)
+                                    s[r][2 * mt + i][e] = fmaf(dk[i][j], c[r][2 * i + e], s[r][2 * mt + i][e]);
                     }
                 }
-                // ------------------------------------ value scales ----
-                const bool edge = t0 + kUnit > L - (a.Tq - 1);    // some row's positions end in this unit
-                uint32_t vw[4][2][NB / 2];
-                uint32_t mxw = 0;
+                if (t0 + kUnit > L - (a.Tq - 1)) {    // some row's positions end in this unit
 #pragma unroll
-                for (int nt = 0; nt < 4; nt++) {
-                    scale_words<NB>(vw[nt], vsb + (8 * nt + 2 * t4) * NB * 2);
-                    if (edge) {
-                        const int p = t0 + 8 * nt + 2 * t4;
+                    for (int p = 0; p < 4; p++)
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
+                        for (int r = 0; r < NT; r++)
 #pragma unroll
-                            for (int i = 0; i < NB / 2; i++)
-                                vw[nt][e][i] = p + e < L ? vw[nt][e][i] : 0u;
-#pragma unroll
-                            for (int r = 0; r < NT; r++)
-                                s[r][nt][e] = p + e < lim[r] ? s[r][nt][e] : -INFINITY;
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; e++)
-#pragma unroll
-                        for (int i = 0; i < NB / 2; i++)
-                            mxw = __vmaxu2(mxw, vw[nt][e][i]);
+                            for (int e = 0; e < 2; e++)
+                                s[r][p][e] = t0 + 8 * p + g < lim[r][e] ? s[r][p][e] : -INFINITY;
                 }
                 // --------------------------------- running reference ----
-                // the lane's bound on log2(dV), and per row on s + log2(dV) - kBase
-                const float eb = fmaf((float)max(mxw & 0x7fffu, (mxw >> 16) & 0x7fffu), 0x1p-10f, -15.0f - kBase);
+                // the unit's bound on log2(dV), and per row on s + log2(dV) - kBase
+                const float eb = fmaf((float)vmax, 0x1p-10f, -15.0f - kBase);
                 bool grow = false;
-                float cand[NT];
+                float cand[NT][2];
 #pragma unroll
-                for (int r = 0; r < NT; r++) {
-                    float mx = s[r][0][0];
+                for (int r = 0; r < NT; r++)
 #pragma unroll
-                    for (int i = 1; i < 8; i++)
-                        mx = fmaxf(mx, s[r][i >> 1][i & 1]);
-                    mx = __fadd_ru(mx, eb);           // (rounded up: scores of any size keep p dV in range)
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    cand[r] = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    grow = grow || cand[r] - m[r] > kSlack;
-                }
+                    for (int e = 0; e < 2; e++) {
+                        float mx = fmaxf(fmaxf(s[r][0][e], s[r][1][e]), fmaxf(s[r][2][e], s[r][3][e]));
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                        cand[r][e] = __fmaf_ru(mx, mul[r][e], eb);   // (rounded up: scores of any size keep p dV in range)
+                        grow = grow || cand[r][e] - m[r][e] > kSlack;
+                    }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                    for (int r = 0; r < NT; r++) {
-                        const float mn = fmaxf(m[r], cand[r]);
-                        const float f = ex2(m[r] - mn);
-                        m[r] = mn;
-                        l[r] *= f;
-                        // accumulator columns are rows 2 t4 and 2 t4 + 1 of the tile
-                        const float f0 = __shfl_sync(0xffffffffu, f, 8 * t4), f1 = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+                    for (int r = 0; r < NT; r++)
 #pragma unroll
-                        for (int i = 0; i < 2 * NB; i++) {
-                            acc[r][i][0] *= f0;
-                            acc[r][i][1] *= f1;
-                            acc[r][i][2] *= f0;
-                            acc[r][i][3] *= f1;
+                        for (int e = 0; e < 2; e++) {
+                            const float mn = fmaxf(m[r][e], cand[r][e]), f = ex2(m[r][e] - mn);
+                            m[r][e] = mn;
+                            l[r][e] *= f;
+#pragma unroll
+                            for (int i = 0; i < 2 * NB; i++) {
+                                acc[r][i][e] *= f;
+                                acc[r][i][e + 2] *= f;
+                            }
                         }
-                    }
                 }
 #pragma unroll
                 for (int r = 0; r < NT; r++)
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        float &p = s[r][i >> 1][i & 1];
-                        p = ex2(p - m[r]);
-                        l[r] += p;
-                    }
+                    for (int p = 0; p < 4; p++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            float &w = s[r][p][e];
+                            w = ex2(fmaf(w, mul[r][e], -m[r][e]));
+                            l[r][e] += w;
+                        }
                 // ------------------------------------------ values ----
 #pragma unroll
                 for (int k = 0; k < 2; k++) {         // 16 positions
+                    float dv[2][NB];
+                    row_scales<NB>(dv[0], conv + (kUnit + 16 * k + g) * NB * 4);
+                    row_scales<NB>(dv[1], conv + (kUnit + 16 * k + 8 + g) * NB * 4);
 #pragma unroll
                     for (int j2 = 0; j2 < NB / 2; j2++) {
                         uint32_t x[4];                // block 2 j2: positions 0-7, 8-15; block 2 j2 + 1
@@ -512,17 +561,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                             const int j = 2 * j2 + jj;
                             uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-                            for (int hf = 0; hf < 2; hf++) {
-                                const uint32_t w0 = vw[2 * k + hf][0][j2], w1 = vw[2 * k + hf][1][j2];
-                                const float d0 = jj ? f16_hi(w0) : f16_lo(w0), d1 = jj ? f16_hi(w1) : f16_lo(w1);
+                            for (int r = 0; r < NT; r++)
 #pragma unroll
-                                for (int r = 0; r < NT; r++) {
-                                    const float p0 = s[r][2 * k + hf][0] * d0, p1 = s[r][2 * k + hf][1] * d1;
-                                    bh[r][hf] = pack_f16x2(p0, p1);
+                                for (int i = 0; i < 2; i++) {
+                                    const float p0 = s[r][2 * k + i][0] * dv[i][j], p1 = s[r][2 * k + i][1] * dv[i][j];
+                                    const uint32_t w = pack_f16x2(p0, p1);
+                                    bh[r][i] = transposed(w);
                                     if constexpr (kTwo)
-                                        bl[r][hf] = pack_f16x2(p0 - f16_lo(bh[r][hf]), p1 - f16_hi(bh[r][hf]));
+                                        bl[r][i] = transposed(pack_f16x2(p0 - f16_lo(w), p1 - f16_hi(w)));
                                 }
-                            }
                             const uint32_t x0 = x[2 * jj], x1 = x[2 * jj + 1], y0 = x0 >> 8, y1 = x1 >> 8;
                             const uint32_t e0 = nib_lo(x0), e1 = nib_hi(x0), e2 = nib_lo(x1), e3 = nib_hi(x1);
                             const uint32_t f0 = nib_lo(y0), f1 = nib_hi(y0), f2 = nib_lo(y1), f3 = nib_hi(y1);
@@ -540,31 +587,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 }
             }
             __syncwarp();
-            if (issued < total) {                     // refill the slot just read
-                if (lane == 0)
-                    issue();
-                issued++;
-                advance(is);
-            }
-            cur.t++;
+            issue(kb);                                // refill the slot just read
+            kb += C::kSlotBytes;
+            if (kb == ring + C::kRing)
+                kb = ring;
         }
-        if (!ok)
-            break;
         // ---------------------------------------------- segment's end ----
 #pragma unroll
-        for (int r = 0; r < NT; r++) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        }
-        const bool before = st0 > 0, after = st0 + (ue - (u - (cur.t - st0))) < snu;
+        for (int r = 0; r < NT; r++)
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], off);
+        const bool before = st0 > 0, after = t0 < snu * kUnit;
         if (!before && !after) {
             if (!idle) {
 #pragma unroll
                 for (int r = 0; r < NT; r++) {
-                    const float inv = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
 #pragma unroll
                     for (int c = 0; c < 2; c++) {
-                        const float fi = __shfl_sync(0xffffffffu, inv, 8 * t4 + 4 * c);
+                        const float fi = l[r][c] > 0.0f ? 1.0f / l[r][c] : 0.0f;
                         const int row = row_base + 8 * r + 2 * t4 + c;
                         if (row < a.R) {
                             O *o = static_cast<O *>(a.o) +
@@ -583,14 +626,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             // slot; one that only continues after it is the share's last, and
             // the ring is drained
             float *pp = before ? first_part : last_part;
-            const Entry e = {sb, shp, u - (cur.t - st0) - st0, snu};
-            if (before) {
-                ent_first = e;
-                any_first = true;
-            } else {
-                ent_last = e;
-                any_last = true;
-            }
+            if (lane == 0 && rgi == 0)
+                entry[2 * wk + (before ? 0 : 1)] = {sb, shp, u - t0 / kUnit, snu};
 #pragma unroll
             for (int r = 0; r < NT; r++) {
 #pragma unroll
@@ -602,28 +639,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                         *reinterpret_cast<float2 *>(o + 32 * j + 16 + 2 * g) = make_float2(acc[r][2 * j][c + 2], acc[r][2 * j + 1][c + 2]);
                     }
                 }
-                if (t4 == 0) {
-                    pp[C::kRows * C::kLd + 8 * r + g] = m[r];
-                    pp[C::kRows * C::kLd + C::kRows + 8 * r + g] = l[r];
-                }
+                if (g == 0)
+                    *reinterpret_cast<float4 *>(pp + C::kRows * C::kLd + 2 * (8 * r + 2 * t4)) =
+                        make_float4(m[r][0], l[r][0], m[r][1], l[r][1]);
             }
         }
         // the next segment
         cur.t = 0;
         if (!after && ++cur.hp == HP)
             next_seq(cur);
-    }
-    if (!ok) {                                        // copies in flight land before the CTA ends
-        if (lane == 0 && a.status)
-            atomicOr(a.status, kStatusTimeout);
-        for (int i = n; i < issued; i++)
-            (void)mbar_wait_bounded(smem_u32(&bar_full[warp][i % S]), (i / S) & 1);
-    }
-    if (lane == 0 && rgi == 0) {
-        if (any_first)
-            entry[wk][0] = ent_first;
-        if (any_last)
-            entry[wk][1] = ent_last;
     }
     __syncthreads();
 
@@ -636,120 +660,136 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                (((size_t)e.b * a.Tq + rr / a.G) * a.Hkv * a.G + (size_t)(e.hp / a.passes) * a.G + rr % a.G) * D;
     };
     auto live_rows = [&](const Entry &e) { return min(rows_cta, a.R - (e.hp % a.passes) * kPassRows); };
-    Entry shared_seg[2];
-    int n_shared = 0;
-    for (int i = 0; i < 2 * NW;) {
-        const Entry e = entry[i >> 1][i & 1];
-        if (e.b < 0) {
-            i++;
-            continue;
-        }
-        int last = i;
-        for (int k = i + 1; k < 2 * NW; k++) {
-            const Entry f = entry[k >> 1][k & 1];
-            if (f.b < 0)
-                continue;
-            if (f.b != e.b || f.hp != e.hp)
-                break;
-            last = k;
-        }
+    // Entries of one segment are consecutive (the invalid ones skipped): a group
+    // is worker wa's entry and the first entry of each following worker.
+    Entry mine = {-1, 0, 0, 0};
+    if (lane < 2 * NW)
+        mine = entry[lane];
+    const unsigned valid = __ballot_sync(0xffffffffu, mine.b >= 0);
+    const unsigned earlier = valid & ((1u << lane) - 1u);
+    const int prev_first = __shfl_sync(0xffffffffu, mine.first, earlier ? 31 - __clz(earlier) : 0);
+    const unsigned heads = __ballot_sync(0xffffffffu, mine.b >= 0 && (!earlier || prev_first != mine.first));
+    auto group_of = [&](int i) {                      // the entries of the group headed by entry i
+        const unsigned after = heads & ~((2u << i) - 1u);
+        return valid & ~((1u << i) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : ~0u);
+    };
+    auto entry_part = [&](int k, int rq) -> const float * {
+        const int w = (k >> 1) * a.rg + rq;
+        return (k & 1) ? reinterpret_cast<const float *>(sbase + w * C::kRing)
+                       : reinterpret_cast<const float *>(sbase + W * C::kRing) + w * C::kPart;
+    };
+    int shared_seg[2], n_shared = 0;                  // head entries of segments other CTAs share
+    for (unsigned hm = heads; hm; hm &= hm - 1) {
+        const int i = __ffs(hm) - 1;
+        const Entry e = entry[i];
+        const int wa = i >> 1, wb = (31 - __clz(group_of(i))) >> 1;
         const bool whole = e.first >= r0 && e.first + e.units <= r1;
-        const int gslot = e.first < r0 ? 0 : 1;
-        float *gpart = a.partials + ((size_t)cta * 2 + gslot) * gp;
+        float *gpart = a.partials + ((size_t)cta * 2 + (e.first < r0 ? 0 : 1)) * gp;
         const int rows = live_rows(e);
-        for (int it = threadIdx.x; it < rows * (D / 2); it += C::kThreads) {
-            const int row = it / (D / 2), d = it % (D / 2) * 2;
+        for (int it = threadIdx.x; it < rows * (D / 4); it += C::kThreads) {
+            const int row = it / (D / 4), d = it % (D / 4) * 4;
             const int rq = row / C::kRows, rr = row % C::kRows;
-            float M = kFloor, Ls = 0.0f, o0 = 0.0f, o1 = 0.0f;
-            for (int k = i; k <= last; k++) {
-                if (entry[k >> 1][k & 1].b < 0)
-                    continue;
-                const int w = (k >> 1) * a.rg + rq;
-                const float *pp = (k & 1) ? reinterpret_cast<const float *>(sbase + w * C::kRing)
-                                          : reinterpret_cast<const float *>(sbase + W * C::kRing) + w * C::kPart;
-                const float mk = pp[C::kRows * C::kLd + rr], lk = pp[C::kRows * C::kLd + C::kRows + rr];
-                const float2 ok2 = *reinterpret_cast<const float2 *>(pp + rr * C::kLd + d);
-                const float Mn = fmaxf(M, mk), fo = ex2(M - Mn), fk = ex2(mk - Mn);
-                M = Mn;
-                Ls = Ls * fo + lk * fk;
-                o0 = o0 * fo + ok2.x * fk;
-                o1 = o1 * fo + ok2.y * fk;
+            const float *pa = entry_part(i, rq);
+            // worker wa's entry, then the first entries of wa + 1 .. wb
+            const float *pf = reinterpret_cast<const float *>(sbase + W * C::kRing) + rq * C::kPart;
+            const int step = a.rg * C::kPart, ml = C::kRows * C::kLd + 2 * rr;
+            float M = pa[ml];
+#pragma unroll 4
+            for (int w = wa + 1; w <= wb; w++)
+                M = fmaxf(M, pf[w * step + ml]);
+            float L = 0.0f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int w = wa; w <= wb; w++) {
+                const float *pp = w == wa ? pa : pf + w * step;
+                const float2 s2 = *reinterpret_cast<const float2 *>(pp + ml);
+                const float4 v = *reinterpret_cast<const float4 *>(pp + rr * C::kLd + d);
+                const float f = ex2(s2.x - M);
+                L = fmaf(f, s2.y, L);
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+                o.z = fmaf(f, v.z, o.z);
+                o.w = fmaf(f, v.w, o.w);
             }
             if (whole) {
-                const float inv = Ls > 0.0f ? 1.0f / Ls : 0.0f;
-                store2(out_row(e, row) + d, o0 * inv, o1 * inv);
+                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                store4(out_row(e, row) + d, o, inv);
             } else {
-                __stcg(reinterpret_cast<float2 *>(gpart + (size_t)row * D + d), make_float2(o0, o1));
-                if (d == 0) {
-                    __stcg(gpart + (size_t)rows_cta * D + row, M);
-                    __stcg(gpart + (size_t)rows_cta * (D + 1) + row, Ls);
-                }
+                __stcg(reinterpret_cast<float4 *>(gpart + (size_t)row * D + d), o);
+                if (d == 0)
+                    __stcg(reinterpret_cast<float2 *>(gpart + (size_t)rows_cta * D) + row, make_float2(M, L));
             }
         }
         if (!whole && n_shared < 2)
-            shared_seg[n_shared++] = e;
-        i = last + 1;
+            shared_seg[n_shared++] = i;
     }
     if (n_shared == 0)
         return;
 
     // --------------------------------------------------- merge the CTAs ----
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x < n_shared) {
-        const Entry e = threadIdx.x == 0 ? shared_seg[0] : shared_seg[1];
-        const int cf = owner_of(e.first, U, n_act), cl = owner_of(e.first + e.units - 1, U, n_act);
+    if ((int)threadIdx.x < n_shared) {
+        const Entry e = entry[shared_seg[threadIdx.x]];
+        const int cf = sh.owner(e.first), cl = sh.owner(e.first + e.units - 1);
+        __threadfence();                              // (the barrier above orders the whole CTA's partial before it)
         arrived[threadIdx.x] = atom_add_acq_rel_gpu(a.counters + cf, 1) == cl - cf;
+        __threadfence();
     }
     __syncthreads();
     for (int k = 0; k < n_shared; k++) {
         if (!arrived[k])
             continue;
-        __threadfence();
-        const Entry e = k == 0 ? shared_seg[0] : shared_seg[1];
-        const int cf = owner_of(e.first, U, n_act), cl = owner_of(e.first + e.units - 1, U, n_act);
-        // the segment starts inside cf (its second slot) and before every later CTA (their first)
-        auto part = [&](int c) { return a.partials + ((size_t)c * 2 + (c == cf ? 1 : 0)) * gp; };
+        const Entry e = entry[shared_seg[k]];
+        const int cf = sh.owner(e.first), cl = sh.owner(e.first + e.units - 1);
         const int rows = live_rows(e);
-        for (int it = threadIdx.x; it < rows * (D / 2); it += C::kThreads) {
-            const int row = it / (D / 2), d = it % (D / 2) * 2;
-            float M = kFloor, Ls = 0.0f, o0 = 0.0f, o1 = 0.0f;
-            for (int c0 = cf; c0 <= cl; c0 += 8) {    // 8 partials' loads in flight
-                float mc[8], lc[8];
-                float2 oc[8];
+        // The segment starts inside cf (its second slot) and before every later
+        // CTA (their first slots, 2 gp apart).
+        float *base = a.partials + (size_t)cf * 2 * gp;
+        constexpr int kBatch = 8;                     // partials whose loads are in flight together
+        for (int it = threadIdx.x; it < rows * (D / 4); it += C::kThreads) {
+            const int row = it / (D / 4), d = it % (D / 4) * 4;
+            float M = kFloor, L = 0.0f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c0 = cf; c0 <= cl; c0 += kBatch) {
+                float2 s2[kBatch];
+                float4 v[kBatch];
+                const float *pc = base + (size_t)(c0 - cf) * 2 * gp;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const bool in = c0 + i <= cl;
-                    const float *pc = part(in ? c0 + i : cf);
-                    mc[i] = in ? __ldcg(pc + (size_t)rows_cta * D + row) : kFloor;
-                    lc[i] = in ? __ldcg(pc + (size_t)rows_cta * (D + 1) + row) : 0.0f;
-                    oc[i] = in ? __ldcg(reinterpret_cast<const float2 *>(pc + (size_t)row * D + d)) : make_float2(0.f, 0.f);
+                for (int i = 0; i < kBatch; i++) {
+                    s2[i] = make_float2(kFloor, 0.0f);
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c0 + i <= cl) {
+                        const float *p = pc + (c0 + i == cf ? gp : 0);
+                        s2[i] = __ldcg(reinterpret_cast<const float2 *>(p + (size_t)rows_cta * D) + row);
+                        v[i] = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)row * D + d));
+                    }
+                    pc += 2 * gp;
                 }
                 float Mn = M;
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    Mn = fmaxf(Mn, mc[i]);
+                for (int i = 0; i < kBatch; i++)
+                    Mn = fmaxf(Mn, s2[i].x);
                 const float fo = ex2(M - Mn);
                 M = Mn;
-                Ls *= fo;
-                o0 *= fo;
-                o1 *= fo;
+                L *= fo;
+                o.x *= fo, o.y *= fo, o.z *= fo, o.w *= fo;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float f = ex2(mc[i] - Mn);
-                    Ls = fmaf(f, lc[i], Ls);
-                    o0 = fmaf(f, oc[i].x, o0);
-                    o1 = fmaf(f, oc[i].y, o1);
+                for (int i = 0; i < kBatch; i++) {
+                    const float f = ex2(s2[i].x - Mn);
+                    L = fmaf(f, s2[i].y, L);
+                    o.x = fmaf(f, v[i].x, o.x);
+                    o.y = fmaf(f, v[i].y, o.y);
+                    o.z = fmaf(f, v[i].z, o.z);
+                    o.w = fmaf(f, v[i].w, o.w);
                 }
             }
-            const float inv = Ls > 0.0f ? 1.0f / Ls : 0.0f;
-            store2(out_row(e, row) + d, o0 * inv, o1 * inv);
+            store4(out_row(e, row) + d, o, L > 0.0f ? 1.0f / L : 0.0f);
         }
         __syncthreads();                              // every partial is read: leave the workspace zero
-        for (int c = cf; c <= cl; c++) {
-            float *pc = part(c);
-            for (size_t i = threadIdx.x * 2; i < gp; i += C::kThreads * 2)
-                __stcg(reinterpret_cast<float2 *>(pc + i), make_float2(0.f, 0.f));
+        for (int c = cf + warp; c <= cl; c += W) {
+            float4 *pc = reinterpret_cast<float4 *>(base + (size_t)(c - cf) * 2 * gp + (c == cf ? gp : 0));
+            for (int i = lane; i < (int)gp / 4; i += 32)
+                __stcg(pc + i, make_float4(0.f, 0.f, 0.f, 0.f));
         }
         if (threadIdx.x == 0)
             a.counters[cf] = 0;
@@ -819,19 +859,14 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
         return BQ_ERR_ALIGN;
     if (ws_bytes < need)
         return BQ_ERR_WORKSPACE;
+    (void)dev_status;                                 // nothing here can fail on the device
     const int sms = device_sm_count();
     if (sms <= 0)
         return BQ_ERR_CUDA;
     aq::Args a;
     memset(&a, 0, sizeof(a));
-    const uint64_t dims[2] = {(uint64_t)kv->D / 2, (uint64_t)rows}, stride[1] = {(uint64_t)kv->D / 2};
-    const uint32_t box[2] = {(uint32_t)kv->D / 2, (uint32_t)aq::kUnit};
-    const CUtensorMapSwizzle sw = kv->D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-    if (!encode_tensor_map(&a.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv->k_codes, dims, stride, box, sw,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-        !encode_tensor_map(&a.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv->v_codes, dims, stride, box, sw,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-        return BQ_ERR_CUDA;
+    a.kc = kv->k_codes;
+    a.vc = kv->v_codes;
     a.ks = kv->k_scales;
     a.vs = kv->v_scales;
     a.q = q;
@@ -848,7 +883,6 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     a.scale2 = scale * 1.4426950408889634f;
     a.counters = static_cast<int *>(ws);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + aq::kMaxGrid * sizeof(int));
-    a.status = dev_status;
     const int grid = sms < aq::kMaxGrid ? sms : aq::kMaxGrid;
     const bool f16 = o_dtype == BQ_F16;
     if (kv->D == 128) {
