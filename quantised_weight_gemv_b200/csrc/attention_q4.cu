@@ -54,8 +54,10 @@ namespace bq {
 namespace aq {
 
 constexpr int kUnit = 32;                 // positions per unit
-constexpr int kMaxGrid = 256;             // CTAs (one per SM)
+constexpr int kMaxGrid = 160;             // CTAs (one per SM)
 constexpr int kPassRows = 64;             // query rows per pass over a segment (NT = 2)
+constexpr int kMinUnits = 8;              // units per CTA, where there are few
+constexpr int kSnap = 32;                 // segments up to this length are never cut between CTAs (see below)
 constexpr float kFloor = -3.0e38f;        // a reference no score has reached
 constexpr float kBase = 11.0f, kSlack = 4.0f;
 
@@ -73,10 +75,13 @@ struct Cfg {
     static constexpr int kLd = D;                             // floats per row of a partial in shared memory
     static constexpr int kConv = 2 * kUnit * kNB * 4;         // a unit's scales in fp32 (keys, values)
     static constexpr int kPart = kRows * kLd + 2 * kRows;     // floats: O, m, l
-    static constexpr size_t kSmem = 128 + (size_t)kWarps * (kRing + kPart * 4 + kConv);
+    static constexpr int kWarpBytes = kRing + kConv;          // (a multiple of 128); the warps' first partials follow
+    static constexpr size_t kSmem = 128 + (size_t)kWarps * (kWarpBytes + kPart * 4);
     static_assert(kPart * 4 <= kRing, "a warp's last partial fits its drained ring");
     static_assert(kSlotBytes % 128 == 0 && kPart % 4 == 0, "slots and partials keep their alignment");
     static_assert(kSmem <= 227 * 1024 - 1024, "shared memory of an SM");
+    static constexpr int kRoom = kWarps * (kWarpBytes + kPart * 4) / 4 / (D + 2);   // rows of CTA partials that fit there
+    static_assert(kRoom >= 2 * kMaxGrid, "two rows of every CTA's partial");
 };
 
 struct Args {
@@ -117,11 +122,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+// (started at c, whose registers stay)
+__device__ __forceinline__ void mma_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -232,6 +238,14 @@ struct Cursor {
     int b, hp, t, nu;
 };
 
+// A CTA's share of the line, made by its first warp.
+struct Plan {
+    int n_act;                            // CTAs with work
+    int split;                            // 1: the CTA's segment has CTAs of its own, cf .. cl
+    int r0, r1, cf, cl;                   // its units (split: counted from the segment's start)
+    Shares line, workers;                 // even shares of the line and of r0 .. r1
+};
+
 template <int D, int NT, typename O>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const __grid_constant__ Args a)
 {
@@ -241,14 +255,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     extern __shared__ uint8_t smem_raw[];
     __shared__ Entry entry[2 * W];                    // worker w: 2w (began before its share), 2w + 1
     __shared__ int arrived[2];
+    __shared__ Plan plan;
+    __shared__ Cursor place[W], copy_at[W];           // workers' starts; what each warp copies next
+    __shared__ int2 group[2 * W];                     // first entry, last worker of each merged segment
 
     uint8_t *sbase = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const uint32_t ring = smem_u32(sbase) + warp * C::kRing;
-    float *first_part = reinterpret_cast<float *>(sbase + W * C::kRing) + warp * C::kPart;
-    float *last_part = reinterpret_cast<float *>(sbase + warp * C::kRing);
-    const uint32_t conv = smem_u32(sbase) + W * (C::kRing + C::kPart * 4) + warp * C::kConv;
-    const int HP = a.Hkv * a.passes;
+    uint8_t *const mine_raw = sbase + warp * C::kWarpBytes;
+    const uint32_t ring = smem_u32(mine_raw), conv = ring + C::kRing;
+    float *const last_part = reinterpret_cast<float *>(mine_raw);
+    float *const first_part = reinterpret_cast<float *>(sbase + W * C::kWarpBytes) + warp * C::kPart;
+    const int HP = a.Hkv * a.passes, cta = blockIdx.x;
+    const int NW = W / a.rg, wk = warp / a.rg, rgi = warp - wk * a.rg;   // workers: rg warps, one per row group
 
     if (threadIdx.x < W * 2)
         entry[threadIdx.x].b = -1;
@@ -258,48 +276,124 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     auto length = [&](int b) { return min(max(a.lens[b], 0), a.Tmax); };
     auto units_of = [&](int b) { return (length(b) + kUnit - 1) / kUnit; };
 
-    // -------- prefix sums of the units per sequence (of one head and pass):
-    // lane i holds the sum before its chunk of sequences ----
-    const int chunk = (a.B + 31) / 32;
-    int before_chunk, U;
-    {
-        int sum = 0;
-        const int b1 = min(a.B, (lane + 1) * chunk);
-#pragma unroll 4
-        for (int b = lane * chunk; b < b1; b++)
-            sum += units_of(b);
-        int inc = sum;
+    if (warp == 0) {
+        // ------------------------------ how the CTAs share the units ----
+        // lane i sums over its chunk of sequences (of one head and pass)
+        const int chunk = (a.B + 31) / 32, b0 = lane * chunk, b1 = min(a.B, b0 + chunk), n_cta = gridDim.x;
+        int sum = 0, some = 0;
+#pragma unroll 1
+        for (int b = b0; b < b1; b++) {
+            const int n = units_of(b);
+            sum += n;
+            some += n > 0;
+        }
+        const int U = __reduce_add_sync(0xffffffffu, sum) * HP;
+        const long long N = (long long)__reduce_add_sync(0xffffffffu, some) * HP;
+        // Split: every segment has CTAs of its own, ceil(units / T) of them, if
+        // that takes no more than the grid with T at most 24 units (3/16) above
+        // an even share.  Otherwise the line is cut evenly (below), and a CTA that
+        // shares two segments merges twice, 3 us more, the time of 24 units:
+        // 16.5 against 13.5 us at 8 segments of 256 units; but 68 us cut evenly
+        // against 73 at 64 segments of 1024 units, where T would be 69 more.
+        int T = max(kMinUnits, (U + n_cta - 1) / n_cta);
+        bool split = false;
+        if (N <= n_cta) {
+            const int more = min((T + 15) >> 4, 8);
+#pragma unroll 1
+            for (int i = 0; i < 4 && !split; i++) {
+                int k = 0;
+                for (int b = b0; b < b1; b++)
+                    k += (units_of(b) + T - 1) / T;
+                split = __reduce_add_sync(0xffffffffu, k) * HP <= n_cta;
+                if (split)
+                    sum = k;                          // CTAs instead of units, from here on
+                else
+                    T += more;
+            }
+        }
+        int before = sum;                             // of the chunks before the lane's
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            const int v = __shfl_up_sync(0xffffffffu, before, off);
             if (lane >= off)
-                inc += v;
+                before += v;
         }
-        before_chunk = inc - sum;
-        U = __shfl_sync(0xffffffffu, inc, 31) * HP;
+        const int all = __shfl_sync(0xffffffffu, before, 31) * HP;
+        before -= sum;
+        Plan pl;
+        pl.n_act = split ? all : min(n_cta, (U + kMinUnits - 1) / kMinUnits);
+        pl.split = split;
+        // Item x (a CTA of a split, else a unit; each lane its own): its sequence,
+        // head-pass, and number within them.
+        auto items_of = [&](int nu) { return split ? (nu + T - 1) / T : nu; };
+        auto locate = [&](int x) {
+            int ci = 0;                               // the chunk holding it: the last that begins at or before it
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                const int v = __shfl_sync(0xffffffffu, before, ci + off);
+                if ((ci + off) * chunk < a.B && v * HP <= x)
+                    ci += off;
+            }
+            int left = x - __shfl_sync(0xffffffffu, before, ci) * HP;
+            Cursor c = {ci * chunk, 0, 0, 0};
+            int per = 0;
+            for (; c.b < a.B; c.b++) {
+                c.nu = units_of(c.b);
+                per = items_of(c.nu);
+                if (left < per * HP)
+                    break;
+                left -= per * HP;
+            }
+            per = max(per, 1);
+            c.hp = left / per;
+            c.t = left - c.hp * per;
+            return c;
+        };
+        if (cta < pl.n_act) {
+            Cursor c;
+            pl.line = {U / pl.n_act, U % pl.n_act};
+            if (split) {                              // units counted from the segment's start
+                c = locate(cta);
+                const int k = items_of(c.nu), part = c.t;
+                const Shares sp = {c.nu / k, c.nu % k};
+                pl.r0 = sp.start(part), pl.r1 = sp.start(part + 1);
+                pl.cf = cta - part, pl.cl = pl.cf + k - 1;
+            } else {
+                // A cut inside a short segment moves to its nearer end: 16 units
+                // more at most, against a merge across CTAs.  (Lane 0: the
+                // share's start, lane 1: its end.)
+                int x = pl.line.start(min(cta + lane, pl.n_act));
+                c = locate(min(x, U - 1));
+                if (x < U && c.nu <= kSnap)
+                    x += 2 * c.t < c.nu ? -c.t : c.nu - c.t;
+                pl.r0 = __shfl_sync(0xffffffffu, x, 0), pl.r1 = __shfl_sync(0xffffffffu, x, 1);
+                pl.cf = pl.cl = 0;
+            }
+            // (workers without units, if any, are the CTA's last: the merge counts on it)
+            pl.workers = {(pl.r1 - pl.r0) / NW, (pl.r1 - pl.r0) % NW};
+            const int w0 = pl.r0 + pl.workers.start(min(lane, NW));
+            if (split)
+                c.t = w0;
+            else
+                c = locate(min(w0, U - 1));
+            if (lane < NW)
+                place[lane] = c;
+        }
+        if (lane == 0)
+            plan = pl;
+    } else {
+        // ------------------------------- sequences without positions ----
+        for (int b = cta; b < a.B; b += gridDim.x)
+            if (length(b) == 0) {
+                const size_t n = (size_t)a.R * a.Hkv * D;
+                O *o = static_cast<O *>(a.o) + b * n;
+                for (size_t i = (threadIdx.x - 32) * 2; i < n; i += (C::kThreads - 32) * 2)
+                    store2(o + i, 0.0f, 0.0f);
+            }
     }
-    // workers; a worker is rg (1, 2, 4) warps, one per row group
-    const int rg_log = a.rg >> 1, nw_log = (W == 16 ? 4 : 3) - rg_log, NW = 1 << nw_log;
-    const int n_act = min((int)gridDim.x, (U + NW - 1) >> nw_log);
-    const int cta = blockIdx.x;
-
-    // -------- sequences without positions ----
-    for (int b = cta; b < a.B; b += gridDim.x)
-        if (length(b) == 0) {
-            const size_t n = (size_t)a.R * a.Hkv * D;
-            O *o = static_cast<O *>(a.o) + b * n;
-            for (size_t i = threadIdx.x * 2; i < n; i += C::kThreads * 2)
-                store2(o + i, 0.0f, 0.0f);
-        }
-    if (cta >= n_act)
+    __syncthreads();
+    if (cta >= plan.n_act)
         return;
-    const Shares sh = {U / n_act, U % n_act};
-    const int r0 = sh.start(cta), r1 = sh.start(cta + 1);
-    const int wk = warp >> rg_log, rgi = warp & (a.rg - 1);
-    // (workers without units, if any, are the CTA's last: the merge counts on it)
-    const Shares ws = {(r1 - r0) >> nw_log, (r1 - r0) & (NW - 1)};
-    const int w0 = r0 + ws.start(wk), w1 = r0 + ws.start(wk + 1);
-
     auto next_seq = [&](Cursor &c) {                  // the next sequence with units
         c.hp = 0;
         do {
@@ -307,18 +401,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             c.nu = c.b < a.B ? units_of(c.b) : 1;
         } while (c.nu == 0);
     };
-    Cursor cur = {0, 0, 0, 1};
-    if (w0 < w1) {
-        // the chunk holding unit w0: the last that begins at or before it
-        const unsigned m1 = __ballot_sync(0xffffffffu, lane * chunk < a.B && before_chunk * HP <= w0);
-        const int ci = 31 - __clz(m1);
-        int left = w0 - __shfl_sync(0xffffffffu, before_chunk, ci) * HP;
-        cur.b = ci * chunk - 1;
-        for (next_seq(cur); left >= cur.nu * HP; next_seq(cur))
-            left -= cur.nu * HP;
-        cur.hp = left / cur.nu;
-        cur.t = left % cur.nu;
-    }
+    const int w0 = plan.r0 + plan.workers.start(wk), w1 = plan.r0 + plan.workers.start(wk + 1);
+    Cursor cur = place[wk];
 
     // ------------------------------------------------------- the ring ----
     // row groups past the last row have nothing to do
@@ -329,7 +413,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     constexpr int kSc = C::kScales / 16;              // lanes per scale plane: 16 or 8
     const uint32_t lane_dst = swizzled<D>(lane / NB, lane % NB);
     // what is copied next: position row `is_row` of the planes, `is_left` units of its segment, `to_issue` in all
-    Cursor is = cur;
+    if (lane == 0)
+        copy_at[warp] = cur;
+    __syncwarp();
     int is_left = cur.nu - cur.t, to_issue = w1 - w0;
     auto seg_row = [&](const Cursor &c) { return (c.b * a.Hkv + (a.passes == 1 ? c.hp : c.hp / a.passes)) * a.Tmax; };
     int is_row = seg_row(cur) + cur.t * kUnit;
@@ -348,18 +434,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             to_issue--;
             is_row += kUnit;
             if (--is_left == 0) {
-                if (++is.hp == HP)
-                    next_seq(is);
-                is_left = is.nu;
-                is_row = seg_row(is);
+                Cursor c = copy_at[warp];
+                if (++c.hp == HP)
+                    next_seq(c);
+                is_left = c.nu;
+                is_row = seg_row(c);
+                __syncwarp();
+                if (lane == 0)
+                    copy_at[warp] = c;
+                __syncwarp();
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int k = 0; k < S; k++)
-        issue(ring + k * C::kSlotBytes);
-
     // ------------------------------------------------------ the stream ----
     uint32_t kb = ring;                               // slot of the unit at hand
     int u = w0;
@@ -374,23 +461,35 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         // nibbles); the lane's row is g of each tile.  What follows a score is
         // held for the accumulator's rows, 2 t4 + e.
         uint32_t qf[NT][NB][2][2];
-        float mul[NT][2], koff[NT][NB][2];
+        float mul[NT][2], koff[NT][NB][4];
         int lim[NT][2];                               // positions a row sees
+        uint2 v[NT][NB][2];
+        int tok[NT];
 #pragma unroll
         for (int r = 0; r < NT; r++) {
             const int row = row_base + g + 8 * r;
             const bool live = row < a.R;
-            const int tok = live ? row / a.G : 0;
-            const uint16_t *qp = a.q + (((size_t)sb * a.Tq + tok) * a.Hkv * a.G + (size_t)h * a.G + (live ? row % a.G : 0)) * D;
-            uint2 v[NB][2];
+            tok[r] = live ? row / a.G : 0;
+            const uint16_t *qp = a.q + (((size_t)sb * a.Tq + tok[r]) * a.Hkv * a.G + (size_t)h * a.G + (live ? row - tok[r] * a.G : 0)) * D;
+#pragma unroll
+            for (int j = 0; j < NB; j++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++)
+                    v[r][j][hf] = live ? *reinterpret_cast<const uint2 *>(qp + 32 * j + 16 * hf + 4 * t4) : make_uint2(0u, 0u);
+        }
+        if (u == w0) {                                // (the first copies queue behind the query, not before it)
+#pragma unroll
+            for (int k = 0; k < S; k++)
+                issue(ring + k * C::kSlotBytes);
+        }
+#pragma unroll
+        for (int r = 0; r < NT; r++) {
             uint32_t mx = 0;
 #pragma unroll
             for (int j = 0; j < NB; j++)
 #pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    v[j][hf] = live ? *reinterpret_cast<const uint2 *>(qp + 32 * j + 16 * hf + 4 * t4) : make_uint2(0u, 0u);
-                    mx = __vmaxu2(mx, __vmaxu2(v[j][hf].x & 0x7fff7fffu, v[j][hf].y & 0x7fff7fffu));
-                }
+                for (int hf = 0; hf < 2; hf++)
+                    mx = __vmaxu2(mx, __vmaxu2(v[r][j][hf].x & 0x7fff7fffu, v[r][j][hf].y & 0x7fff7fffu));
             mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             const int top = (int)max(mx & 0xffffu, mx >> 16);
@@ -402,23 +501,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 mul[r][e] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4 * e);
-                lim[r][e] = L - (a.Tq - 1 - __shfl_sync(0xffffffffu, tok, 8 * t4 + 4 * e));
+                lim[r][e] = L - (a.Tq - 1 - __shfl_sync(0xffffffffu, tok[r], 8 * t4 + 4 * e));
             }
 #pragma unroll
             for (int j = 0; j < NB; j++) {
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                float (&z)[4] = koff[r][j];
+                z[0] = z[1] = z[2] = z[3] = 0.0f;
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
                     const float fh = hf ? f * 0.0625f : f;
                     // register e holds elements 4 t4 + e and 4 t4 + 2 + e: the order of the masked key bytes
-                    qf[r][j][hf][0] = pack_f16x2(f16_lo(v[j][hf].x) * fh, f16_lo(v[j][hf].y) * fh);
-                    qf[r][j][hf][1] = pack_f16x2(f16_hi(v[j][hf].x) * fh, f16_hi(v[j][hf].y) * fh);
+                    qf[r][j][hf][0] = pack_f16x2(f16_lo(v[r][j][hf].x) * fh, f16_lo(v[r][j][hf].y) * fh);
+                    qf[r][j][hf][1] = pack_f16x2(f16_hi(v[r][j][hf].x) * fh, f16_hi(v[r][j][hf].y) * fh);
                     // -8 2^-24 (-128 2^-24) as fp16 subnormals
                     const uint32_t zp = hf ? 0x80808080u : 0x80088008u;
                     mma(z, zp, zp, zp, zp, qf[r][j][hf][0], qf[r][j][hf][1]);
                 }
-                koff[r][j][0] = z[0];
-                koff[r][j][1] = z[1];
             }
         }
         float m[NT][2], l[NT][2], acc[NT][2 * NB][4];
@@ -464,16 +562,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
                         row_scales<NB>(dk[i], conv + (16 * mt + 8 * i + g) * NB * 4);
-#pragma unroll
-                        for (int r = 0; r < NT; r++)
-#pragma unroll
-                            for (int e = 0; e < 2; e++) {
-                                float z = dk[i][0] * koff[r][0][e];
-#pragma unroll
-                                for (int j = 1; j < NB; j++)
-                                    z = fmaf(dk[i][j], koff[r][j][e], z);
-                                s[r][2 * mt + i][e] = z;
-                            }
                     }
 #pragma unroll
                     for (int j = 0; j < NB; j++) {
@@ -481,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                         float c[NT][4];
 #pragma unroll
                         for (int r = 0; r < NT; r++)
-                            mma0(c[r], x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu,
+                            mma_from(c[r], koff[r][j], x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu,
                                  qf[r][j][0][0], qf[r][j][0][1]);
 #pragma unroll
                         for (int r = 0; r < NT; r++)
@@ -493,7 +581,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                             for (int i = 0; i < 2; i++)
 #pragma unroll
                                 for (int e = 0; e < 2; e++)
-                                    s[r][2 * mt + i][e] = fmaf(dk[i][j], c[r][2 * i + e], s[r][2 * mt + i][e]);
+                                    s[r][2 * mt + i][e] = j == 0 ? dk[i][0] * c[r][2 * i + e]
+                                                                 : fmaf(dk[i][j], c[r][2 * i + e], s[r][2 * mt + i][e]);
                     }
                 }
                 if (t0 + kUnit > L - (a.Tq - 1)) {    // some row's positions end in this unit
@@ -675,53 +764,59 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     };
     auto entry_part = [&](int k, int rq) -> const float * {
         const int w = (k >> 1) * a.rg + rq;
-        return (k & 1) ? reinterpret_cast<const float *>(sbase + w * C::kRing)
-                       : reinterpret_cast<const float *>(sbase + W * C::kRing) + w * C::kPart;
+        return reinterpret_cast<const float *>(sbase + ((k & 1) ? w * C::kWarpBytes : W * C::kWarpBytes + w * C::kPart * 4));
     };
-    int shared_seg[2], n_shared = 0;                  // head entries of segments other CTAs share
-    for (unsigned hm = heads; hm; hm &= hm - 1) {
-        const int i = __ffs(hm) - 1;
+    if (warp == 0 && (heads >> lane & 1)) {
+        const int k = __popc(heads & ((1u << lane) - 1u));
+        group[k] = make_int2(lane, (31 - __clz(group_of(lane))) >> 1);
+    }
+    __syncthreads();
+    const int n_groups = __popc(heads), items = rows_cta * (D / 4);
+#pragma unroll 1
+    for (int it = threadIdx.x; it < n_groups * items; it += C::kThreads) {
+        const int k = it / items, row = it % items / (D / 4), d = it % (D / 4) * 4;
+        const int i = group[k].x, wb = group[k].y, wa = i >> 1;
         const Entry e = entry[i];
-        const int wa = i >> 1, wb = (31 - __clz(group_of(i))) >> 1;
-        const bool whole = e.first >= r0 && e.first + e.units <= r1;
-        float *gpart = a.partials + ((size_t)cta * 2 + (e.first < r0 ? 0 : 1)) * gp;
-        const int rows = live_rows(e);
-        for (int it = threadIdx.x; it < rows * (D / 4); it += C::kThreads) {
-            const int row = it / (D / 4), d = it % (D / 4) * 4;
-            const int rq = row / C::kRows, rr = row % C::kRows;
-            const float *pa = entry_part(i, rq);
-            // worker wa's entry, then the first entries of wa + 1 .. wb
-            const float *pf = reinterpret_cast<const float *>(sbase + W * C::kRing) + rq * C::kPart;
-            const int step = a.rg * C::kPart, ml = C::kRows * C::kLd + 2 * rr;
-            float M = pa[ml];
+        if (row >= live_rows(e))
+            continue;
+        const int rq = row / C::kRows, rr = row % C::kRows;
+        const float *pa = entry_part(i, rq);
+        // worker wa's entry, then the first entries of wa + 1 .. wb
+        const float *pf = entry_part(0, rq);
+        const int step = a.rg * C::kPart, ml = C::kRows * C::kLd + 2 * rr;
+        float M = pa[ml];
+#pragma unroll 8
+        for (int w = wa + 1; w <= wb; w++)
+            M = fmaxf(M, pf[w * step + ml]);
+        float L = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int w = wa + 1; w <= wb; w++)
-                M = fmaxf(M, pf[w * step + ml]);
-            float L = 0.0f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int w = wa; w <= wb; w++) {
-                const float *pp = w == wa ? pa : pf + w * step;
-                const float2 s2 = *reinterpret_cast<const float2 *>(pp + ml);
-                const float4 v = *reinterpret_cast<const float4 *>(pp + rr * C::kLd + d);
-                const float f = ex2(s2.x - M);
-                L = fmaf(f, s2.y, L);
-                o.x = fmaf(f, v.x, o.x);
-                o.y = fmaf(f, v.y, o.y);
-                o.z = fmaf(f, v.z, o.z);
-                o.w = fmaf(f, v.w, o.w);
-            }
-            if (whole) {
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-                store4(out_row(e, row) + d, o, inv);
-            } else {
-                __stcg(reinterpret_cast<float4 *>(gpart + (size_t)row * D + d), o);
-                if (d == 0)
-                    __stcg(reinterpret_cast<float2 *>(gpart + (size_t)rows_cta * D) + row, make_float2(M, L));
-            }
+        for (int w = wa; w <= wb; w++) {
+            const float *pp = w == wa ? pa : pf + w * step;
+            const float2 s2 = *reinterpret_cast<const float2 *>(pp + ml);
+            const float4 v = *reinterpret_cast<const float4 *>(pp + rr * C::kLd + d);
+            const float f = ex2(s2.x - M);
+            L = fmaf(f, s2.y, L);
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
         }
-        if (!whole && n_shared < 2)
-            shared_seg[n_shared++] = i;
+        if (e.first >= plan.r0 && e.first + e.units <= plan.r1) {
+            store4(out_row(e, row) + d, o, L > 0.0f ? 1.0f / L : 0.0f);
+        } else {
+            float *gpart = a.partials + ((size_t)cta * 2 + (e.first < plan.r0 ? 0 : 1)) * gp;
+            __stcg(reinterpret_cast<float4 *>(gpart + (size_t)row * D + d), o);
+            if (d == 0)
+                __stcg(reinterpret_cast<float2 *>(gpart + (size_t)rows_cta * D) + row, make_float2(M, L));
+        }
+    }
+    // segments other CTAs share: the first and the last group may be
+    int shared_seg[2], n_shared = 0;
+    for (int k = 0; k < n_groups; k += max(1, n_groups - 1)) {
+        const Entry e = entry[group[k].x];
+        if (e.first < plan.r0 || e.first + e.units > plan.r1)
+            shared_seg[n_shared++] = group[k].x;
     }
     if (n_shared == 0)
         return;
@@ -730,66 +825,75 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     __syncthreads();
     if ((int)threadIdx.x < n_shared) {
         const Entry e = entry[shared_seg[threadIdx.x]];
-        const int cf = sh.owner(e.first), cl = sh.owner(e.first + e.units - 1);
-        __threadfence();                              // (the barrier above orders the whole CTA's partial before it)
+        const int cf = plan.split ? plan.cf : plan.line.owner(e.first);
+        const int cl = plan.split ? plan.cl : plan.line.owner(e.first + e.units - 1);
+        // (release and acquire for the whole CTA: the barriers on both sides extend it to the other threads)
         arrived[threadIdx.x] = atom_add_acq_rel_gpu(a.counters + cf, 1) == cl - cf;
-        __threadfence();
     }
     __syncthreads();
     for (int k = 0; k < n_shared; k++) {
         if (!arrived[k])
             continue;
         const Entry e = entry[shared_seg[k]];
-        const int cf = sh.owner(e.first), cl = sh.owner(e.first + e.units - 1);
+        const int cf = plan.split ? plan.cf : plan.line.owner(e.first);
+        const int cl = plan.split ? plan.cl : plan.line.owner(e.first + e.units - 1);
         const int rows = live_rows(e);
         // The segment starts inside cf (its second slot) and before every later
-        // CTA (their first slots, 2 gp apart).
+        // CTA (their first slots, 2 gp apart).  (Cuts inside segments that CTAs
+        // share are where the even shares put them: owner() holds there.)
         float *base = a.partials + (size_t)cf * 2 * gp;
-        constexpr int kBatch = 8;                     // partials whose loads are in flight together
-        for (int it = threadIdx.x; it < rows * (D / 4); it += C::kThreads) {
-            const int row = it / (D / 4), d = it % (D / 4) * 4;
-            float M = kFloor, L = 0.0f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c0 = cf; c0 <= cl; c0 += kBatch) {
-                float2 s2[kBatch];
-                float4 v[kBatch];
-                const float *pc = base + (size_t)(c0 - cf) * 2 * gp;
-#pragma unroll
-                for (int i = 0; i < kBatch; i++) {
-                    s2[i] = make_float2(kFloor, 0.0f);
-                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c0 + i <= cl) {
-                        const float *p = pc + (c0 + i == cf ? gp : 0);
-                        s2[i] = __ldcg(reinterpret_cast<const float2 *>(p + (size_t)rows_cta * D) + row);
-                        v[i] = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)row * D + d));
-                    }
-                    pc += 2 * gp;
-                }
-                float Mn = M;
-#pragma unroll
-                for (int i = 0; i < kBatch; i++)
-                    Mn = fmaxf(Mn, s2[i].x);
-                const float fo = ex2(M - Mn);
-                M = Mn;
-                L *= fo;
-                o.x *= fo, o.y *= fo, o.z *= fo, o.w *= fo;
-#pragma unroll
-                for (int i = 0; i < kBatch; i++) {
-                    const float f = ex2(s2[i].x - Mn);
-                    L = fmaf(f, s2[i].y, L);
-                    o.x = fmaf(f, v[i].x, o.x);
-                    o.y = fmaf(f, v[i].y, o.y);
-                    o.z = fmaf(f, v[i].z, o.z);
-                    o.w = fmaf(f, v[i].w, o.w);
-                }
+        // All partials of a few rows are copied to shared memory at once (the
+        // rings and the warps' partials are done with) and summed there; warps without a sum, or all after
+        // it, clear what was copied.  Loops, not unrolled: this runs once, and
+        // fetching its code is what it would cost.
+        const int P = cl - cf + 1;
+        const int step = min(32, (C::kRoom / P) & ~1);   // (even, at least 2)
+        float *so = reinterpret_cast<float *>(sbase);
+        for (int row0 = 0; row0 < rows; row0 += step) {
+            const int nr = min(step, rows - row0), n4 = nr * (D / 4), nr2 = (nr + 1) & ~1;
+            float2 *sml = reinterpret_cast<float2 *>(so + P * nr * D);
+#pragma unroll 1
+            for (int p = warp; p < P; p += W) {
+                const float *src = base + (size_t)p * 2 * gp + (p == 0 ? gp : 0);
+#pragma unroll 1
+                for (int i = lane; i < n4; i += 32)
+                    copy16(smem_u32(so + (p * n4 + i) * 4), src + (size_t)row0 * D + i * 4);
+                if (2 * lane < nr)
+                    copy16(smem_u32(sml + p * nr2 + 2 * lane), src + (size_t)rows_cta * D + (row0 + 2 * lane) * 2);
             }
-            store4(out_row(e, row) + d, o, L > 0.0f ? 1.0f / L : 0.0f);
-        }
-        __syncthreads();                              // every partial is read: leave the workspace zero
-        for (int c = cf + warp; c <= cl; c += W) {
-            float4 *pc = reinterpret_cast<float4 *>(base + (size_t)(c - cf) * 2 * gp + (c == cf ? gp : 0));
-            for (int i = lane; i < (int)gp / 4; i += 32)
-                __stcg(pc + i, make_float4(0.f, 0.f, 0.f, 0.f));
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+#pragma unroll 1
+            for (int it = threadIdx.x; it < nr * (D / 2); it += C::kThreads) {
+                const int row = it / (D / 2), d = it % (D / 2) * 2;
+                float M = kFloor, L = 0.0f;
+                float2 o = make_float2(0.f, 0.f);
+#pragma unroll 4
+                for (int p = 0; p < P; p++)
+                    M = fmaxf(M, sml[p * nr2 + row].x);
+#pragma unroll 4
+                for (int p = 0; p < P; p++) {
+                    const float2 s2 = sml[p * nr2 + row];
+                    const float2 v = *reinterpret_cast<const float2 *>(so + (p * nr + row) * D + d);
+                    const float f = ex2(s2.x - M);
+                    L = fmaf(f, s2.y, L);
+                    o.x = fmaf(f, v.x, o.x);
+                    o.y = fmaf(f, v.y, o.y);
+                }
+                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                store2(out_row(e, row0 + row) + d, o.x * inv, o.y * inv);
+            }
+            const int busy = (nr * (D / 2) + 31) / 32, from = busy < W ? busy : 0;
+#pragma unroll 1
+            for (int p = warp - from; p >= 0 && p < P; p += W - from) {
+                float *src = base + (size_t)p * 2 * gp + (p == 0 ? gp : 0);
+#pragma unroll 1
+                for (int i = lane; i < n4; i += 32)
+                    __stcg(reinterpret_cast<float4 *>(src + (size_t)row0 * D) + i, make_float4(0.f, 0.f, 0.f, 0.f));
+                if (2 * lane < nr)
+                    __stcg(reinterpret_cast<float4 *>(src + (size_t)rows_cta * D + row0 * 2) + lane, make_float4(0.f, 0.f, 0.f, 0.f));
+            }
+            __syncthreads();                          // (the space is free again)
         }
         if (threadIdx.x == 0)
             a.counters[cf] = 0;
