@@ -266,7 +266,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     float *const last_part = reinterpret_cast<float *>(mine_raw);
     float *const first_part = reinterpret_cast<float *>(sbase + W * C::kWarpBytes) + warp * C::kPart;
     const int HP = a.Hkv * a.passes, cta = blockIdx.x;
-    const int NW = W / a.rg, wk = warp / a.rg, rgi = warp - wk * a.rg;   // workers: rg warps, one per row group
+    // workers: rg (1, 2, 4) warps each, one per row group
+    const int rg_log = a.rg >> 1, nw_log = (W == 16 ? 4 : 3) - rg_log, NW = 1 << nw_log;
+    const int wk = warp >> rg_log, rgi = warp & (a.rg - 1);
 
     if (threadIdx.x < W * 2)
         entry[threadIdx.x].b = -1;
@@ -295,22 +297,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         // shares two segments merges twice, 3 us more, the time of 24 units:
         // 16.5 against 13.5 us at 8 segments of 256 units; but 68 us cut evenly
         // against 73 at 64 segments of 1024 units, where T would be 69 more.
-        int T = max(kMinUnits, (U + n_cta - 1) / n_cta);
-        bool split = false;
+        // (Divisions are a tenth of a microsecond each here; T and the CTAs of a
+        // segment need not be exact, only the same in every CTA.)
+        const int T = max(kMinUnits, (int)((float)U / (float)n_cta) + 1);
+        float per_T = 0.0f;                           // 1 / T of a split, else 0
+        auto split_ctas = [](int nu, float inv) { return nu == 0 ? 0 : max(1, min(nu, (int)(nu * inv + 0.99f))); };
         if (N <= n_cta) {
             const int more = min((T + 15) >> 4, 8);
-#pragma unroll 1
-            for (int i = 0; i < 4 && !split; i++) {
-                int k = 0;
-                for (int b = b0; b < b1; b++)
-                    k += (units_of(b) + T - 1) / T;
-                split = __reduce_add_sync(0xffffffffu, k) * HP <= n_cta;
-                if (split)
-                    sum = k;                          // CTAs instead of units, from here on
-                else
-                    T += more;
+            float inv[4];
+            int k[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                inv[i] = __frcp_rn((float)(T + i * more));
+            for (int b = b0; b < b1; b++) {
+                const int nu = units_of(b);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    k[i] += split_ctas(nu, inv[i]);
             }
+#pragma unroll
+            for (int i = 3; i >= 0; i--)
+                if (__reduce_add_sync(0xffffffffu, k[i]) * HP <= n_cta) {
+                    per_T = inv[i];
+                    some = k[i];
+                }
         }
+        const bool split = per_T > 0.0f;
+        if (split)
+            sum = some;                               // CTAs instead of units, from here on
         int before = sum;                             // of the chunks before the lane's
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -325,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         pl.split = split;
         // Item x (a CTA of a split, else a unit; each lane its own): its sequence,
         // head-pass, and number within them.
-        auto items_of = [&](int nu) { return split ? (nu + T - 1) / T : nu; };
+        auto items_of = [&](int nu) { return split ? split_ctas(nu, per_T) : nu; };
         auto locate = [&](int x) {
             int ci = 0;                               // the chunk holding it: the last that begins at or before it
 #pragma unroll
@@ -344,14 +358,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                     break;
                 left -= per * HP;
             }
-            per = max(per, 1);
-            c.hp = left / per;
+            if (HP > 1) {
+                per = max(per, 1);
+                c.hp = left / per;
+            }
             c.t = left - c.hp * per;
             return c;
         };
         if (cta < pl.n_act) {
             Cursor c;
-            pl.line = {U / pl.n_act, U % pl.n_act};
             if (split) {                              // units counted from the segment's start
                 c = locate(cta);
                 const int k = items_of(c.nu), part = c.t;
@@ -359,6 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 pl.r0 = sp.start(part), pl.r1 = sp.start(part + 1);
                 pl.cf = cta - part, pl.cl = pl.cf + k - 1;
             } else {
+                pl.line = {U / pl.n_act, U % pl.n_act};
                 // A cut inside a short segment moves to its nearer end: 16 units
                 // more at most, against a merge across CTAs.  (Lane 0: the
                 // share's start, lane 1: its end.)
@@ -370,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 pl.cf = pl.cl = 0;
             }
             // (workers without units, if any, are the CTA's last: the merge counts on it)
-            pl.workers = {(pl.r1 - pl.r0) / NW, (pl.r1 - pl.r0) % NW};
+            pl.workers = {(pl.r1 - pl.r0) >> nw_log, (pl.r1 - pl.r0) & (NW - 1)};
             const int w0 = pl.r0 + pl.workers.start(min(lane, NW));
             if (split)
                 c.t = w0;
@@ -453,7 +469,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     while (u < w1) {
         const int sb = cur.b, shp = cur.hp, st0 = cur.t, snu = cur.nu;
         const int ue = min(w1, u + snu - st0);
-        const int h = shp / a.passes, row_base = (shp % a.passes) * kPassRows + rgi * 16;
+        const int pass = a.passes == 1 ? 0 : shp % a.passes, h = a.passes == 1 ? shp : shp / a.passes;
+        const int row_base = pass * kPassRows + rgi * 16;
         const int L = length(sb);
         const bool idle = idle_pass(shp);
 
@@ -469,7 +486,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         for (int r = 0; r < NT; r++) {
             const int row = row_base + g + 8 * r;
             const bool live = row < a.R;
-            tok[r] = live ? row / a.G : 0;
+            tok[r] = live && a.Tq > 1 ? row / a.G : 0;
             const uint16_t *qp = a.q + (((size_t)sb * a.Tq + tok[r]) * a.Hkv * a.G + (size_t)h * a.G + (live ? row - tok[r] * a.G : 0)) * D;
 #pragma unroll
             for (int j = 0; j < NB; j++)
@@ -743,12 +760,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     // ------------------------------------------------ merge the workers ----
     const int rows_cta = C::kRows * a.rg;             // rows of a pass
     const size_t gp = (size_t)rows_cta * (D + 2);     // floats of a CTA partial
+    auto pass_of = [&](const Entry &e) { return a.passes == 1 ? 0 : e.hp % a.passes; };
     auto out_row = [&](const Entry &e, int row) {     // output of a pass's row (row < R checked by the caller)
-        const int rr = (e.hp % a.passes) * kPassRows + row;
-        return static_cast<O *>(a.o) +
-               (((size_t)e.b * a.Tq + rr / a.G) * a.Hkv * a.G + (size_t)(e.hp / a.passes) * a.G + rr % a.G) * D;
+        const int rr = pass_of(e) * kPassRows + row, tok = a.Tq == 1 ? 0 : rr / a.G;
+        return static_cast<O *>(a.o) + (((size_t)e.b * a.Tq + tok) * a.Hkv * a.G +
+                                        (size_t)(a.passes == 1 ? e.hp : e.hp / a.passes) * a.G + (rr - tok * a.G)) * D;
     };
-    auto live_rows = [&](const Entry &e) { return min(rows_cta, a.R - (e.hp % a.passes) * kPassRows); };
+    auto live_rows = [&](const Entry &e) { return min(rows_cta, a.R - pass_of(e) * kPassRows); };
     // Entries of one segment are consecutive (the invalid ones skipped): a group
     // is worker wa's entry and the first entry of each following worker.
     Entry mine = {-1, 0, 0, 0};
@@ -771,10 +789,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         group[k] = make_int2(lane, (31 - __clz(group_of(lane))) >> 1);
     }
     __syncthreads();
-    const int n_groups = __popc(heads), items = rows_cta * (D / 4);
+    constexpr int kItemsLog = (NT == 1 ? 3 : 4) + (D == 128 ? 5 : 4);     // of a row group: kRows * D / 4
+    const int n_groups = __popc(heads), items_log = kItemsLog + rg_log;
 #pragma unroll 1
-    for (int it = threadIdx.x; it < n_groups * items; it += C::kThreads) {
-        const int k = it / items, row = it % items / (D / 4), d = it % (D / 4) * 4;
+    for (int it = threadIdx.x; it < n_groups << items_log; it += C::kThreads) {
+        const int k = it >> items_log, row = (it & ((1 << items_log) - 1)) / (D / 4), d = it % (D / 4) * 4;
         const int i = group[k].x, wb = group[k].y, wa = i >> 1;
         const Entry e = entry[i];
         if (row >= live_rows(e))
