@@ -346,6 +346,20 @@ def _one_device(fn: str, **tensors) -> None:
             raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{cur}")
 
 
+_T = None          # torch, its dtypes' codes and current stream's address, once a call has needed them
+
+
+def _torch():
+    global _T
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # (current_stream() takes 3 us)
+    if raw is None:
+        def raw(dev):
+            return torch.cuda.current_stream(dev).cuda_stream
+    _T = (torch, {torch.float32: BQ_F32, torch.float16: BQ_F16, torch.bfloat16: BQ_BF16}, raw)
+    return _T
+
+
 def kv_cache_q4(k_codes, k_scales, v_codes, v_scales) -> bq_kv_cache_q4:
     """A bq_kv_cache_q4 over device tensors: codes uint8 [B, Hkv, Tmax, D/2],
     scales fp16 (bits) [B, Hkv, Tmax, D/32], keys and values alike (the tensors
@@ -368,7 +382,7 @@ def kv_cache_q4(k_codes, k_scales, v_codes, v_scales) -> bq_kv_cache_q4:
 
 
 def _dtype_code(fn: str, t) -> int:
-    code = {"torch.float32": BQ_F32, "torch.float16": BQ_F16, "torch.bfloat16": BQ_BF16}.get(str(t.dtype))
+    code = (_T or _torch())[1].get(t.dtype)
     if code is None:
         raise ValueError(f"{fn}: dtype {t.dtype} is not float32, float16 or bfloat16")
     return code
@@ -385,9 +399,28 @@ def _overlaps(shape, strides) -> bool:
     return False
 
 
-def _kv_rows(fn: str, kv, k, v, start, count, status, write: bool) -> bq_kv_rows:
-    """Checks rows k, v ([B, T, Hkv, D] over the cache kv), start and count
-    (int32 [B]); write: the rows are destinations (one of them may be None)."""
+def _rows_struct(k, v, dtype: int, T: int) -> bq_kv_rows:
+    # (a stride over an extent of 1 is never used)
+    if T > 1:
+        kb, kt, kh = (0, 0, 0) if k is None else k.stride()[:3]
+        vb, vt, vh = (0, 0, 0) if v is None else v.stride()[:3]
+    else:
+        kt = vt = 0
+        kb, _, kh = (0, 0, 0) if k is None else k.stride()[:3]
+        vb, _, vh = (0, 0, 0) if v is None else v.stride()[:3]
+    t = k if k is not None else v
+    if t.shape[0] == 1:
+        kb = vb = 0
+    if t.shape[2] == 1:
+        kh = vh = 0
+    return bq_kv_rows(0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
+                      kb, kt, kh, vb, vt, vh, dtype, T)
+
+
+def _refuse_rows(fn: str, kv, k, v, start, count, status, write: bool) -> None:
+    """Raises for what is wrong with rows k, v ([B, T, Hkv, D] over the cache
+    kv), start or count (int32 [B]); write: the rows are destinations (one of
+    them may be None)."""
     if not isinstance(kv, (bq_kv_cache, bq_kv_cache_q4)) or not hasattr(kv, "B"):
         raise ValueError(f"{fn}: kv must come from kv_cache or kv_cache_q4")
     given = [t for t in (k, v) if t is not None]
@@ -408,12 +441,45 @@ def _kv_rows(fn: str, kv, k, v, start, count, status, write: bool) -> bq_kv_rows
     for name, t in (("start", start), ("count", count)):
         if t is not None and (t.numel() != kv.B or str(t.dtype) != "torch.int32" or not t.is_contiguous()):
             raise ValueError(f"{fn}: {name} must be int32 [{kv.B}]")
-    dt = _dtype_code(fn, given[0])
-
-    def strides(t):                  # a stride over an extent of 1 is never used
-        return [0, 0, 0] if t is None else [s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])]
+    if status is not None and (status.element_size() != 4 or status.numel() < 1):
+        raise ValueError(f"{fn}: status must hold an int32")
+    _dtype_code(fn, given[0])
     _one_device(fn, cache=kv._refs[0], k=k, v=v, start=start, count=count, status=status)
-    return bq_kv_rows(_ptr(k), _ptr(v), *strides(k), *strides(v), dt, int(T))
+
+
+def _kv_rows_call(fn: str, kv, k, v, start, count, status, stream, write: bool) -> None:
+    # One pass over what has to hold (this runs once a layer and token); what
+    # does not is named by _refuse_rows.
+    torch, codes, raw_stream = _T or _torch()
+    try:
+        t = v if k is None else k
+        B, T, H, D = t.shape
+        dtype = codes[t.dtype]
+        dev = kv._refs[0].get_device()
+        good = (dev >= 0 and B == kv.B and H == kv.Hkv and D == kv.D and T > 0 and t.stride(3) == 1
+                and (v is None or v is t or (v.shape == t.shape and v.dtype is t.dtype and v.stride(3) == 1))
+                and (write or (k is not None and v is not None))
+                and (not write or ((k is None or k.is_contiguous() or not _overlaps(k.shape, k.stride()))
+                                   and (v is None or v.is_contiguous() or not _overlaps(v.shape, v.stride()))))
+                and start.dtype is torch.int32 and start.numel() == B and start.is_contiguous()
+                and (count is None or (count.dtype is torch.int32 and count.numel() == B and count.is_contiguous()
+                                       and count.get_device() == dev))
+                and (status is None or (status.get_device() == dev and status.element_size() == 4
+                                        and status.numel() > 0))
+                and t.get_device() == dev and (v is None or v.get_device() == dev) and start.get_device() == dev
+                and torch.cuda.current_device() == dev)
+    except (AttributeError, KeyError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_rows(fn, kv, k, v, start, count, status, write)
+    rows = _rows_struct(k, v, dtype, T)
+    name = ("bq_kv_read_q" if write else "bq_kv_append_q") + ("4" if isinstance(kv, bq_kv_cache_q4) else "8")
+    rc = getattr(_lib or lib(), name)(ctypes.byref(kv), ctypes.byref(rows), B, H, start.data_ptr(),
+                                      None if count is None else count.data_ptr(),
+                                      None if status is None else status.data_ptr(),
+                                      raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check(name, rc)
 
 
 def kv_append(kv, k, v, start, count=None, status=None, stream=None) -> None:
@@ -421,20 +487,31 @@ def kv_append(kv, k, v, start, count=None, status=None, stream=None) -> None:
     contiguous rows) into positions start[b] .. start[b] + count[b] - 1 of the
     cache (count None: T rows each), through bq_kv_append_q4 or _q8 as kv is a
     Q4 or a Q8 cache.  start and count are int32 [B] on the device."""
-    rows = _kv_rows("kv_append", kv, k, v, start, count, status, False)
-    name = "bq_kv_append_q4" if isinstance(kv, bq_kv_cache_q4) else "bq_kv_append_q8"
-    check(name, getattr(lib(), name)(ctypes.byref(kv), ctypes.byref(rows), kv.B, kv.Hkv, start.data_ptr(),
-                                     _ptr(count), _ptr(status), _stream_ptr(stream)))
+    _kv_rows_call("kv_append", kv, k, v, start, count, status, stream, False)
 
 
 def kv_read(kv, k, v, start, count=None, status=None, stream=None) -> None:
     """Read positions start[b] .. start[b] + count[b] - 1 of the cache into rows
     k, v ([B, T, Hkv, D], fp32 / fp16 / bf16; either may be None) through
     bq_kv_read_q4 or _q8.  Rows from count[b] on are left as they were."""
-    rows = _kv_rows("kv_read", kv, k, v, start, count, status, True)
-    name = "bq_kv_read_q4" if isinstance(kv, bq_kv_cache_q4) else "bq_kv_read_q8"
-    check(name, getattr(lib(), name)(ctypes.byref(kv), ctypes.byref(rows), kv.B, kv.Hkv, start.data_ptr(),
-                                     _ptr(count), _ptr(status), _stream_ptr(stream)))
+    _kv_rows_call("kv_read", kv, k, v, start, count, status, stream, True)
+
+
+def _refuse_attn(kv, q, lens, G, o, ws, status) -> None:
+    if not isinstance(kv, bq_kv_cache_q4) or not hasattr(kv, "B"):
+        raise ValueError("attn_decode_q4: kv must come from kv_cache_q4")
+    _on_device("attn_decode_q4", q=q, lens=lens, o=o, ws=ws, status=status)
+    B, Hkv = kv.B, kv.Hkv
+    want = (B, q.shape[1], Hkv * G, kv.D) if q.dim() == 4 else (B, Hkv * G, kv.D)
+    if tuple(q.shape) != want or q.element_size() != 2 or "bfloat16" in str(q.dtype) or not q.is_contiguous():
+        raise ValueError(f"attn_decode_q4: q must be contiguous fp16 bits [{B}, (Tq,) {Hkv * G}, {kv.D}]")
+    if lens.numel() != B or str(lens.dtype) != "torch.int32" or not lens.is_contiguous():
+        raise ValueError(f"attn_decode_q4: lens must be int32 [{B}]")
+    if tuple(o.shape) != want or _dtype_code("attn_decode_q4", o) == BQ_BF16 or not o.is_contiguous():
+        raise ValueError(f"attn_decode_q4: o must be contiguous float32 or float16 of q's shape {want}")
+    if not ws.is_contiguous():
+        raise ValueError("attn_decode_q4: ws must be contiguous")
+    _one_device("attn_decode_q4", cache=kv._refs[0], q=q, lens=lens, o=o, ws=ws, status=status)
 
 
 def attn_decode_q4(kv: bq_kv_cache_q4, q, lens, G: int, scale: float, o, ws, status=None,
@@ -443,23 +520,30 @@ def attn_decode_q4(kv: bq_kv_cache_q4, q, lens, G: int, scale: float, o, ws, sta
     o are [B, Hkv*G, D] (one query token a sequence) or [B, Tq, Hkv*G, D]; q
     fp16 bits, o fp32 or fp16.  Query token i of sequence b attends to the
     positions below lens[b] - (Tq - 1 - i)."""
-    if not isinstance(kv, bq_kv_cache_q4) or not hasattr(kv, "B"):
-        raise ValueError("attn_decode_q4: kv must come from kv_cache_q4")
-    _on_device("attn_decode_q4", q=q, lens=lens, o=o, ws=ws, status=status)
-    B, Hkv = kv.B, kv.Hkv
-    Tq = q.shape[1] if q.dim() == 4 else 1
-    want = (B, Tq, Hkv * G, kv.D) if q.dim() == 4 else (B, Hkv * G, kv.D)
-    if tuple(q.shape) != want or q.element_size() != 2 or "bfloat16" in str(q.dtype) or not q.is_contiguous():
-        raise ValueError(f"attn_decode_q4: q must be contiguous fp16 bits [{B}, (Tq,) {Hkv * G}, {kv.D}]")
-    if lens.numel() != B or str(lens.dtype) != "torch.int32" or not lens.is_contiguous():
-        raise ValueError(f"attn_decode_q4: lens must be int32 [{B}]")
-    od = _dtype_code("attn_decode_q4", o)
-    if tuple(o.shape) != want or od == BQ_BF16 or not o.is_contiguous():
-        raise ValueError(f"attn_decode_q4: o must be contiguous float32 or float16 of q's shape {want}")
-    _one_device("attn_decode_q4", cache=kv._refs[0], q=q, lens=lens, o=o, ws=ws, status=status)
-    check("bq_attn_decode_q4", lib().bq_attn_decode_q4(
-        ctypes.byref(kv), q.data_ptr(), lens.data_ptr(), B, int(Tq), Hkv, int(G), float(scale), o.data_ptr(),
-        od, ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), _stream_ptr(stream)))
+    torch, codes, raw_stream = _T or _torch()
+    try:
+        shape, dev = q.shape, kv._refs[0].get_device()
+        B, Hkv = kv.B, kv.Hkv
+        Tq = shape[1] if len(shape) == 4 else 1
+        od = codes[o.dtype]
+        good = (dev >= 0 and type(kv) is bq_kv_cache_q4 and len(shape) in (3, 4) and shape[0] == B and shape[-2] == Hkv * G
+                and shape[-1] == kv.D and o.shape == shape and od != BQ_BF16
+                and (q.dtype is torch.float16 or q.dtype is torch.int16 or q.dtype is torch.uint16)
+                and lens.dtype is torch.int32 and lens.numel() == B
+                and q.is_contiguous() and o.is_contiguous() and lens.is_contiguous() and ws.is_contiguous()
+                and q.get_device() == dev and o.get_device() == dev and lens.get_device() == dev
+                and ws.get_device() == dev and (status is None or status.get_device() == dev)
+                and torch.cuda.current_device() == dev)
+    except (AttributeError, KeyError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_attn(kv, q, lens, G, o, ws, status)
+    rc = (_lib or lib()).bq_attn_decode_q4(
+        ctypes.byref(kv), q.data_ptr(), lens.data_ptr(), B, Tq, Hkv, G, scale, o.data_ptr(), od, ws.data_ptr(),
+        ws.numel() * ws.element_size(), None if status is None else status.data_ptr(),
+        raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        check("bq_attn_decode_q4", rc)
 
 
 def moe_gemv_q4(Wstack: bq_qmat, E: int, codes_stride: int, scales_stride: int, x,
