@@ -13,7 +13,7 @@
 // write contiguous sectors, and four rows of one head, whose addresses are one
 // stride apart.  A thread's elements are 4j .. 4j+3 and 16+4j .. 16+4j+3 of its
 // block (j = 0..3): exactly the two nibbles of the Q4 bytes 4j .. 4j+3, one
-// 32-bit word.
+// 32-bit word.  (16-bit rows of the Q8 cache: 8 consecutive elements.)
 //
 // The Q8 cache keeps values transposed ([D][Tmax]), so its value side goes
 // through shared memory in tiles of 64 positions cut at multiples of 64: every
@@ -70,18 +70,22 @@ __device__ __forceinline__ Span span_of(const Args &a, int b)
 }
 
 // ---------------------------------------------------------------- quantise ----
-// A thread's 8 elements of a row, as they are in memory: 4 at p, 4 at p + 16.
-template <typename E>
+// A thread's 8 elements of a row, as they are in memory: 4 at p, 4 at p + GAP
+// (16, or 4: consecutive).
+template <typename E, int GAP>
 struct Raw {
     uint32_t w[2][sizeof(E)];             // 16-bit: 2 words each; fp32: 4
     __device__ __forceinline__ void load(const E *p)
     {
         if constexpr (sizeof(E) == 4) {
-            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p)), b = __ldcs(reinterpret_cast<const uint4 *>(p + 16));
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p)), b = __ldcs(reinterpret_cast<const uint4 *>(p + GAP));
             w[0][0] = a.x, w[0][1] = a.y, w[0][2] = a.z, w[0][3] = a.w;
             w[1][0] = b.x, w[1][1] = b.y, w[1][2] = b.z, w[1][3] = b.w;
+        } else if constexpr (GAP == 4) {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
+            w[0][0] = a.x, w[0][1] = a.y, w[1][0] = a.z, w[1][1] = a.w;
         } else {
-            const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(p)), b = __ldcs(reinterpret_cast<const uint2 *>(p + 16));
+            const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(p)), b = __ldcs(reinterpret_cast<const uint2 *>(p + GAP));
             w[0][0] = a.x, w[0][1] = a.y, w[1][0] = b.x, w[1][1] = b.y;
         }
     }
@@ -137,8 +141,8 @@ struct Raw {
 // |x / d| < L + 0.1 at a normal scale, so codes need no clamp, and adding
 // 1.5 * 2^23 (+ 8) to t leaves the code in the low bits.  Subnormal scales take
 // the careful way, with the clamp.
-template <int FMT, typename E>
-__device__ __forceinline__ bool quantise8(const Raw<E> &raw, uint32_t (&c)[2], uint16_t &scale)
+template <int FMT, typename E, int GAP>
+__device__ __forceinline__ bool quantise8(const Raw<E, GAP> &raw, uint32_t (&c)[2], uint16_t &scale)
 {
     constexpr float kLevels = FMT == 4 ? 7.0f : 127.0f;
     constexpr float kMagic = FMT == 4 ? 12582920.0f : 12582912.0f;
@@ -182,7 +186,7 @@ __device__ __forceinline__ bool quantise8(const Raw<E> &raw, uint32_t (&c)[2], u
     return ok;
 }
 
-// Elements of a thread's place in a row: block and quarter of the block.
+// A thread's place in a Q4 row: block and quarter of the block.
 struct Lane {
     int row, blk, jj;
     template <int D>
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const Args a)
         constexpr int U = ROWS == 1 || sizeof(E) == 4 ? 1 : 2;      // rows whose loads are in flight together
 #pragma unroll 1
         for (int i = i0; i < i0 + ROWS * at_once; i += U * at_once) {
-            Raw<E> x[U][2];
+            Raw<E, 16> x[U][2];
 #pragma unroll
             for (int s = 0; s < U; s++) {
                 x[s][0].load(kp);
@@ -272,9 +276,41 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int b)
     t.hi = w.lo < w.hi ? (int)min(max(end - t.t0, 0LL), (long long)kTile) : 0;
     return t;
 }
-// Word w (positions 4w .. 4w+3) of transposed value row d in a tile of shared
-// memory: the words a warp stores or loads together lie in different banks.
-__device__ __forceinline__ int tile_word(int d, int w) { return d * (kTile / 4) + (w ^ (((d >> 5) << 2) | ((d >> 2) & 3))); }
+// The Q8 kernels' places in a row, for 16 threads j: elements first(j) .. + 3
+// and first(j) + kGap .. + 3.  16-bit rows move 16 bytes at once; fp32 rows keep
+// 4 threads' 16 bytes together (24 against 27 us with 32 bytes a thread, 8 x 4
+// heads x 2.6k positions read).
+template <typename E>
+struct Place {
+    static constexpr int kGap = sizeof(E) == 4 ? 16 : 4;
+    static __device__ __forceinline__ int first(int j) { return kGap == 16 ? 32 * (j >> 2) + 4 * (j & 3) : 8 * j; }
+    // Word w (positions 4w .. 4w+3) of transposed value row d in a tile of shared
+    // memory: the words a warp stores or loads together lie in different banks.
+    static __device__ __forceinline__ int word(int d, int w)
+    {
+        return d * (kTile / 4) + (w ^ (kGap == 16 ? ((d >> 5) << 2) | ((d >> 2) & 3) : d >> 3));
+    }
+};
+
+// Key codes of a thread: 4 bytes at p, 4 at p + GAP.
+template <int GAP>
+__device__ __forceinline__ void store_codes(uint8_t *p, uint32_t lo, uint32_t hi)
+{
+    if constexpr (GAP == 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+    } else {
+        *reinterpret_cast<uint32_t *>(p) = lo;
+        *reinterpret_cast<uint32_t *>(p + GAP) = hi;
+    }
+}
+template <int GAP>
+__device__ __forceinline__ uint2 load_codes(const uint8_t *p)
+{
+    if constexpr (GAP == 4)
+        return __ldcs(reinterpret_cast<const uint2 *>(p));
+    else
+        return make_uint2(__ldcs(reinterpret_cast<const uint32_t *>(p)), __ldcs(reinterpret_cast<const uint32_t *>(p + GAP)));
+}
 
 // One block: 64 positions (a tile cut at a multiple of 64) of one (sequence,
 // head).  Keys go straight to their rows; a thread takes 4 consecutive
@@ -282,44 +318,45 @@ __device__ __forceinline__ int tile_word(int d, int w) { return d * (kTile / 4) 
 // 16 positions (a decode step) take one position a thread and store value bytes
 // where they belong: 3.3 against 5.0 us for a token of 8 x 8 rows.
 template <typename E>
-__global__ void __launch_bounds__(kThreads) append_q8_kernel(const Args a)
+__global__ void __launch_bounds__(kThreads, 3) append_q8_kernel(const Args a)
 {
-    constexpr int D = 128;
+    constexpr int D = 128, kLanes = D / 8, kGap = Place<E>::kGap;
     __shared__ alignas(16) uint32_t vt[D * kTile / 4];
     pdl_launch_dependents();
     pdl_wait();
-    const int h = blockIdx.x % a.Hkv;
-    const Lane l = Lane::of<D>(threadIdx.x);
+    const int h = blockIdx.x % a.Hkv, row = threadIdx.x / kLanes, j = threadIdx.x % kLanes;
+    const int e0 = Place<E>::first(j);
     for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
         const Tile t = tile_of(a, b);
         if (t.lo >= t.hi)
             continue;                                 // (the same for the whole block)
         const size_t bh = (size_t)b * a.Hkv + h;
-        const E *kp = static_cast<const E *>(a.r.k) + b * a.r.k_batch + h * a.r.k_head + l.element();
-        const E *vp = static_cast<const E *>(a.r.v) + b * a.r.v_batch + h * a.r.v_head + l.element();
+        const bool few = t.hi - t.lo <= kThreads / kLanes;
+        const int p0 = few ? t.lo + row : 4 * row;    // the thread's first position
+        // (positions outside the span are read from its nearer end and dropped)
+        const long long i = t.t0 + min(max(p0, t.lo), t.hi - 1) - t.s0;
+        const E *kp = static_cast<const E *>(a.r.k) + b * a.r.k_batch + h * a.r.k_head + i * a.r.k_token + e0;
+        const E *vp = static_cast<const E *>(a.r.v) + b * a.r.v_batch + h * a.r.v_head + i * a.r.v_token + e0;
+        const size_t at = bh * a.Tmax + (size_t)(t.t0 + p0);
+        uint8_t *kc = a.kc + at * D + e0;
+        uint16_t *ks = a.ks + at * (D / 32) + j / 4, *vs = a.vs + at * (D / 32) + j / 4;
         int bits = 0;
-        if (t.hi - t.lo <= kThreads / (D / 8)) {
-            const int p = t.lo + l.row;
-            const bool live = p < t.hi;
-            const long long i = t.t0 + (live ? p : t.lo) - t.s0;
-            Raw<E> x[2];
-            x[0].load(kp + i * a.r.k_token);
-            x[1].load(vp + i * a.r.v_token);
+        if (few) {
+            Raw<E, kGap> x[2];
+            x[0].load(kp);
+            x[1].load(vp);
             uint32_t c[2][2];
             uint16_t sc[2];
             const bool ok = quantise8<8>(x[0], c[0], sc[0]) & quantise8<8>(x[1], c[1], sc[1]);
-            if (live) {
-                const size_t row = bh * a.Tmax + (size_t)(t.t0 + p);
-                uint32_t *dst = reinterpret_cast<uint32_t *>(a.kc + row * D + l.element());
-                dst[0] = c[0][0];
-                dst[4] = c[0][1];
-                uint8_t *out = a.vc + (bh * D + l.element()) * a.Tmax + (size_t)(t.t0 + p);
+            if (p0 < t.hi) {
+                store_codes<kGap>(kc, c[0][0], c[0][1]);
+                uint8_t *out = a.vc + (bh * D + e0) * a.Tmax + (size_t)(t.t0 + p0);
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    out[(size_t)((e & 3) + 16 * (e >> 2)) * a.Tmax] = (uint8_t)(c[1][e >> 2] >> (8 * (e & 3)));
-                if (l.jj == 0) {
-                    a.ks[row * (D / 32) + l.blk] = sc[0];
-                    a.vs[row * (D / 32) + l.blk] = sc[1];
+                    out[(size_t)(e + (e >> 2) * (kGap - 4)) * a.Tmax] = (uint8_t)(c[1][e >> 2] >> (8 * (e & 3)));
+                if (j % 4 == 0) {
+                    *ks = sc[0];
+                    *vs = sc[1];
                 }
                 if (!ok && a.status)
                     atomicOr(a.status, kStatusRange);
@@ -327,32 +364,30 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const Args a)
             continue;
         }
         uint32_t vc[4][2];
-        if ((threadIdx.x / 32 * 2 + 2) * 4 > t.lo && threadIdx.x / 32 * 8 < t.hi) {   // the warp has a position
-            constexpr int U = sizeof(E) == 4 ? 2 : 4;
+        if ((threadIdx.x / 32 + 1) * 8 > t.lo && threadIdx.x / 32 * 8 < t.hi) {   // the warp has a position
+            constexpr int U = sizeof(E) == 4 ? 1 : 2;
 #pragma unroll
             for (int s0 = 0; s0 < 4; s0 += U) {
-                Raw<E> x[U][2];
+                Raw<E, kGap> x[U][2];
 #pragma unroll
-                for (int s = 0; s < U; s++) {
-                    const int p = min(max(4 * l.row + s0 + s, t.lo), t.hi - 1);
-                    const long long i = t.t0 + p - t.s0;
-                    x[s][0].load(kp + i * a.r.k_token);
-                    x[s][1].load(vp + i * a.r.v_token);
+                for (int s = s0; s < s0 + U; s++) {
+                    x[s - s0][0].load(kp);
+                    x[s - s0][1].load(vp);
+                    if (p0 + s >= t.lo && p0 + s + 1 < t.hi) {
+                        kp += a.r.k_token;
+                        vp += a.r.v_token;
+                    }
                 }
 #pragma unroll
-                for (int s = 0; s < U; s++) {
-                    const int p = 4 * l.row + s0 + s;
+                for (int s = s0; s < s0 + U; s++) {
                     uint32_t c[2];
                     uint16_t sc[2];
-                    const bool ok = quantise8<8>(x[s][0], c, sc[0]) & quantise8<8>(x[s][1], vc[s0 + s], sc[1]);
-                    if (p >= t.lo && p < t.hi) {
-                        const size_t row = bh * a.Tmax + (size_t)(t.t0 + p);
-                        uint32_t *dst = reinterpret_cast<uint32_t *>(a.kc + row * D + l.element());
-                        dst[0] = c[0];
-                        dst[4] = c[1];
-                        if (l.jj == 0) {
-                            a.ks[row * (D / 32) + l.blk] = sc[0];
-                            a.vs[row * (D / 32) + l.blk] = sc[1];
+                    const bool ok = quantise8<8>(x[s - s0][0], c, sc[0]) & quantise8<8>(x[s - s0][1], vc[s], sc[1]);
+                    if (p0 + s >= t.lo && p0 + s < t.hi) {
+                        store_codes<kGap>(kc + s * D, c[0], c[1]);
+                        if (j % 4 == 0) {
+                            ks[s * (D / 32)] = sc[0];
+                            vs[s * (D / 32)] = sc[1];
                         }
                         bits |= ok ? 0 : kStatusRange;
                     }
@@ -363,11 +398,11 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const Args a)
             for (int hf = 0; hf < 2; hf++) {
                 const uint32_t x01 = prmt(vc[0][hf], vc[1][hf], 0x5140), y01 = prmt(vc[2][hf], vc[3][hf], 0x5140);
                 const uint32_t x23 = prmt(vc[0][hf], vc[1][hf], 0x7362), y23 = prmt(vc[2][hf], vc[3][hf], 0x7362);
-                const int d = l.element() + 16 * hf;
-                vt[tile_word(d, l.row)] = prmt(x01, y01, 0x5410);
-                vt[tile_word(d + 1, l.row)] = prmt(x01, y01, 0x7632);
-                vt[tile_word(d + 2, l.row)] = prmt(x23, y23, 0x5410);
-                vt[tile_word(d + 3, l.row)] = prmt(x23, y23, 0x7632);
+                const int d = e0 + kGap * hf;
+                vt[Place<E>::word(d, row)] = prmt(x01, y01, 0x5410);
+                vt[Place<E>::word(d + 1, row)] = prmt(x01, y01, 0x7632);
+                vt[Place<E>::word(d + 2, row)] = prmt(x23, y23, 0x5410);
+                vt[Place<E>::word(d + 3, row)] = prmt(x23, y23, 0x7632);
             }
         }
         if (bits && a.status)
@@ -380,7 +415,7 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const Args a)
             if (p + 4 <= t.lo || p >= t.hi)
                 continue;
             uint8_t *out = dst + (size_t)d * a.Tmax + p;
-            const uint32_t v = vt[tile_word(d, p / 4)];
+            const uint32_t v = vt[Place<E>::word(d, p / 4)];
             if (p >= t.lo && p + 4 <= t.hi)
                 *reinterpret_cast<uint32_t *>(out) = v;
             else
@@ -393,9 +428,9 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const Args a)
 }
 
 // -------------------------------------------------------------------- read ----
-// 8 values d * code to a row: x[0..3] at p, x[4..7] at p + 16; d * code is exact
+// 8 values d * code to a row: x[0..3] at p, x[4..7] at p + GAP; d * code is exact
 // in fp32 and rounded once.
-template <typename E>
+template <int GAP, typename E>
 __device__ __forceinline__ void store8(E *p, float d, const float (&x)[8])
 {
     uint32_t w[8];
@@ -413,10 +448,12 @@ __device__ __forceinline__ void store8(E *p, float d, const float (&x)[8])
     }
     if constexpr (sizeof(E) == 4) {
         __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
-        __stcs(reinterpret_cast<uint4 *>(p + 16), make_uint4(w[4], w[5], w[6], w[7]));
+        __stcs(reinterpret_cast<uint4 *>(p + GAP), make_uint4(w[4], w[5], w[6], w[7]));
+    } else if constexpr (GAP == 4) {
+        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
     } else {
         __stcs(reinterpret_cast<uint2 *>(p), make_uint2(w[0], w[1]));
-        __stcs(reinterpret_cast<uint2 *>(p + 16), make_uint2(w[2], w[3]));
+        __stcs(reinterpret_cast<uint2 *>(p + GAP), make_uint2(w[2], w[3]));
     }
 }
 // Codes to fp32: 2^23 + u has u in its low bits.
@@ -475,11 +512,11 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const Args a)
             if (w.has(i0 + s * at_once)) {
                 if (r.k) {
                     codes_q4(c[s][0], x);
-                    store8(kp + s * at_once * r.k_token, f16(sc[s][0]), x);
+                    store8<16>(kp + s * at_once * r.k_token, f16(sc[s][0]), x);
                 }
                 if (r.v) {
                     codes_q4(c[s][1], x);
-                    store8(vp + s * at_once * r.v_token, f16(sc[s][1]), x);
+                    store8<16>(vp + s * at_once * r.v_token, f16(sc[s][1]), x);
                 }
             }
         }
@@ -487,75 +524,82 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const Args a)
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) read_q8_kernel(const Args a)
+__global__ void __launch_bounds__(kThreads, 4) read_q8_kernel(const Args a)
 {
-    constexpr int D = 128;
+    constexpr int D = 128, kLanes = D / 8, kGap = Place<E>::kGap;
     __shared__ alignas(16) uint32_t vt[D * kTile / 4];
     pdl_launch_dependents();
     pdl_wait();
-    const int h = blockIdx.x % a.Hkv;
-    const Lane l = Lane::of<D>(threadIdx.x);
+    const int h = blockIdx.x % a.Hkv, row = threadIdx.x / kLanes, j = threadIdx.x % kLanes;
+    const int e0 = Place<E>::first(j);
     const Rows &r = a.r;
     for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
         const Tile t = tile_of(a, b);
         if (t.lo >= t.hi)
             continue;
         const size_t bh = (size_t)b * a.Hkv + h;
-        E *kp = static_cast<E *>(const_cast<void *>(r.k)) + b * r.k_batch + h * r.k_head + l.element();
-        E *vp = static_cast<E *>(const_cast<void *>(r.v)) + b * r.v_batch + h * r.v_head + l.element();
-        if (t.hi - t.lo <= kThreads / (D / 8)) {      // a position a thread (see append)
-            const int p = t.lo + l.row;
-            if (p >= t.hi)
+        const bool few = t.hi - t.lo <= kThreads / kLanes;   // a position a thread (see append)
+        const int p0 = few ? t.lo + row : 4 * row;
+        const size_t at = bh * a.Tmax + (size_t)(t.t0 + p0);
+        const uint8_t *kc = a.kc + at * D + e0;
+        const uint16_t *ks = a.ks + at * (D / 32) + j / 4, *vs = a.vs + at * (D / 32) + j / 4;
+        const long long i = t.t0 + p0 - t.s0;         // (used where p0 .. are in the span)
+        E *kp = static_cast<E *>(const_cast<void *>(r.k)) + b * r.k_batch + h * r.k_head + i * r.k_token + e0;
+        E *vp = static_cast<E *>(const_cast<void *>(r.v)) + b * r.v_batch + h * r.v_head + i * r.v_token + e0;
+        float x[8];
+        if (few) {
+            if (p0 >= t.hi)
                 continue;
-            const size_t row = bh * a.Tmax + (size_t)(t.t0 + p);
-            const long long i = t.t0 + p - t.s0;
-            float x[8];
             if (r.k) {
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.kc + row * D + l.element());
-                codes_q8(src[0], src[4], x);
-                store8(kp + i * r.k_token, f16(a.ks[row * (D / 32) + l.blk]), x);
+                const uint2 w = load_codes<kGap>(kc);
+                codes_q8(w.x, w.y, x);
+                store8<kGap>(kp, f16(*ks), x);
             }
             if (r.v) {
-                const int8_t *src = reinterpret_cast<const int8_t *>(a.vc) + (bh * D + l.element()) * a.Tmax + (size_t)(t.t0 + p);
+                const int8_t *src = reinterpret_cast<const int8_t *>(a.vc) + (bh * D + e0) * a.Tmax + (size_t)(t.t0 + p0);
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    x[e] = (float)src[(size_t)((e & 3) + 16 * (e >> 2)) * a.Tmax];
-                store8(vp + i * r.v_token, f16(a.vs[row * (D / 32) + l.blk]), x);
+                    x[e] = (float)src[(size_t)(e + (e >> 2) * (kGap - 4)) * a.Tmax];
+                store8<kGap>(vp, f16(*vs), x);
             }
             continue;
         }
-        uint32_t kw[4][2];
+        uint2 kw[4];
         uint16_t sc[4][2];
 #pragma unroll
-        for (int s = 0; s < 4; s++) {
-            const int p = min(max(4 * l.row + s, t.lo), t.hi - 1);
-            const size_t row = bh * a.Tmax + (size_t)(t.t0 + p);
-            if (r.k) {
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.kc + row * D + l.element());
-                kw[s][0] = __ldcs(src);
-                kw[s][1] = __ldcs(src + 4);
-                sc[s][0] = __ldcs(a.ks + row * (D / 32) + l.blk);
+        for (int s = 0; s < 4; s++)
+            if (p0 + s >= t.lo && p0 + s < t.hi) {
+                if (r.k) {
+                    kw[s] = load_codes<kGap>(kc + s * D);
+                    sc[s][0] = __ldcs(ks + s * (D / 32));
+                }
+                if (r.v)
+                    sc[s][1] = __ldcs(vs + s * (D / 32));
             }
-            if (r.v)
-                sc[s][1] = __ldcs(a.vs + row * (D / 32) + l.blk);
-        }
         if (r.v) {
             const uint8_t *src = a.vc + bh * D * a.Tmax + t.t0;   // the whole tile lies inside the plane
 #pragma unroll
             for (int k = 0; k < D * kTile / 4 / kThreads; k++) {
                 const int w = threadIdx.x + k * kThreads, d = w / (kTile / 4), q = w % (kTile / 4);
                 if (4 * q + 4 > t.lo && 4 * q < t.hi)
-                    vt[tile_word(d, q)] = __ldcs(reinterpret_cast<const uint32_t *>(src + (size_t)d * a.Tmax + 4 * q));
+                    vt[Place<E>::word(d, q)] = __ldcs(reinterpret_cast<const uint32_t *>(src + (size_t)d * a.Tmax + 4 * q));
             }
             __syncthreads();
         }
-        uint32_t vc[4][2];
-        if (r.v)
+        if (r.k)
+#pragma unroll
+            for (int s = 0; s < 4; s++)
+                if (p0 + s >= t.lo && p0 + s < t.hi) {
+                    codes_q8(kw[s].x, kw[s].y, x);
+                    store8<kGap>(kp + s * r.k_token, f16(sc[s][0]), x);
+                }
+        if (r.v) {
+            uint32_t vc[4][2];
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) {
-                const int d = l.element() + 16 * hf;
-                const uint32_t e0 = vt[tile_word(d, l.row)], e1 = vt[tile_word(d + 1, l.row)];
-                const uint32_t e2 = vt[tile_word(d + 2, l.row)], e3 = vt[tile_word(d + 3, l.row)];
+                const int d = e0 + kGap * hf;
+                const uint32_t e0 = vt[Place<E>::word(d, row)], e1 = vt[Place<E>::word(d + 1, row)];
+                const uint32_t e2 = vt[Place<E>::word(d + 2, row)], e3 = vt[Place<E>::word(d + 3, row)];
                 const uint32_t x01 = prmt(e0, e1, 0x5140), y01 = prmt(e2, e3, 0x5140);
                 const uint32_t x23 = prmt(e0, e1, 0x7362), y23 = prmt(e2, e3, 0x7362);
                 vc[0][hf] = prmt(x01, y01, 0x5410);
@@ -564,23 +608,13 @@ __global__ void __launch_bounds__(kThreads) read_q8_kernel(const Args a)
                 vc[3][hf] = prmt(x23, y23, 0x7632);
             }
 #pragma unroll
-        for (int s = 0; s < 4; s++) {
-            const int p = 4 * l.row + s;
-            if (p < t.lo || p >= t.hi)
-                continue;
-            const long long i = t.t0 + p - t.s0;
-            float x[8];
-            if (r.k) {
-                codes_q8(kw[s][0], kw[s][1], x);
-                store8(kp + i * r.k_token, f16(sc[s][0]), x);
-            }
-            if (r.v) {
-                codes_q8(vc[s][0], vc[s][1], x);
-                store8(vp + i * r.v_token, f16(sc[s][1]), x);
-            }
-        }
-        if (r.v)
+            for (int s = 0; s < 4; s++)
+                if (p0 + s >= t.lo && p0 + s < t.hi) {
+                    codes_q8(vc[s][0], vc[s][1], x);
+                    store8<kGap>(vp + s * r.v_token, f16(sc[s][1]), x);
+                }
             __syncthreads();
+        }
     }
 }
 
