@@ -55,13 +55,12 @@ namespace aq {
 
 constexpr int kUnit = 32;                 // positions per unit
 constexpr int kMaxGrid = 160;             // CTAs (one per SM)
-constexpr int kPassRows = 64;             // query rows per pass over a segment (NT = 2)
 constexpr int kMinUnits = 8;              // units per CTA, where there are few
 constexpr int kSnap = 32;                 // segments up to this length are never cut between CTAs (see below)
 constexpr float kFloor = -3.0e38f;        // a reference no score has reached
 constexpr float kBase = 11.0f, kSlack = 4.0f;
 
-// D: head width; NT: 8-row tiles per warp (1: R <= 8; 2: 16 rows).
+// D: head width; NT: 8-row tiles per warp (1 or 2: see shape_of).
 template <int D, int NT>
 struct Cfg {
     static constexpr int kNB = D / 32;                        // blocks per row
@@ -91,7 +90,8 @@ struct Args {
     void *o;
     int B, Tq, Hkv, G, Tmax;
     int R;                                // Tq * G query rows per KV head
-    int rg, passes;                       // 16-row groups per CTA (1, 2, 4), passes of 16 rg rows
+    int rg, passes, pass_rows;            // row groups (of 8 NT rows) a CTA takes at once, passes of pass_rows = 8 NT rg rows
+    int rg_inv;                           // warp / rg = warp * rg_inv >> 16
     float scale2;                         // scale * log2(e)
     int *counters;                        // [grid], by a shared segment's first CTA
     float *partials;                      // [grid][2]: O [rows][D], then (m, l) [rows]
@@ -121,6 +121,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // (started at c, whose registers stay)
 __device__ __forceinline__ void mma_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -204,6 +210,12 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t x)
     return h;
 }
 
+// Code pairs as fp16: SIGNED: u - 8; else the masked bits, subnormals u 2^-24 (16 u 2^-24).
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t code_lo(uint32_t x) { return SIGNED ? nib_lo(x) : x & 0x000F000Fu; }
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t code_hi(uint32_t x) { return SIGNED ? nib_hi(x) : x & 0x00F000F0u; }
+
 // Units shared by CTAs: q each, one more for the first r.
 struct Shares {
     int q, r;
@@ -252,6 +264,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     using C = Cfg<D, NT>;
     constexpr int NB = C::kNB, W = C::kWarps, S = C::kSlots;
     constexpr bool kTwo = sizeof(O) == 4;             // p dV as two fp16 terms
+    // Key codes as u - 8 too: the conversion serves both row tiles, and its zero
+    // points would take 32 registers.
+    constexpr bool kSignedK = NT == 2;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Entry entry[2 * W];                    // worker w: 2w (began before its share), 2w + 1
     __shared__ int arrived[2];
@@ -266,9 +281,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     float *const last_part = reinterpret_cast<float *>(mine_raw);
     float *const first_part = reinterpret_cast<float *>(sbase + W * C::kWarpBytes) + warp * C::kPart;
     const int HP = a.Hkv * a.passes, cta = blockIdx.x;
-    // workers: rg (1, 2, 4) warps each, one per row group
-    const int rg_log = a.rg >> 1, nw_log = (W == 16 ? 4 : 3) - rg_log, NW = 1 << nw_log;
-    const int wk = warp >> rg_log, rgi = warp & (a.rg - 1);
+    // workers: rg warps each, one per row group
+    const int NW = (W * a.rg_inv) >> 16, wk = (warp * a.rg_inv) >> 16, rgi = warp - wk * a.rg;
 
     if (threadIdx.x < W * 2)
         entry[threadIdx.x].b = -1;
@@ -386,7 +400,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 pl.cf = pl.cl = 0;
             }
             // (workers without units, if any, are the CTA's last: the merge counts on it)
-            pl.workers = {(pl.r1 - pl.r0) >> nw_log, (pl.r1 - pl.r0) & (NW - 1)};
+            const int each = (pl.r1 - pl.r0) / NW;
+            pl.workers = {each, pl.r1 - pl.r0 - each * NW};
             const int w0 = pl.r0 + pl.workers.start(min(lane, NW));
             if (split)
                 c.t = w0;
@@ -417,12 +432,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             c.nu = c.b < a.B ? units_of(c.b) : 1;
         } while (c.nu == 0);
     };
-    const int w0 = plan.r0 + plan.workers.start(wk), w1 = plan.r0 + plan.workers.start(wk + 1);
-    Cursor cur = place[wk];
+    const int w0 = plan.r0 + plan.workers.start(min(wk, NW)), w1 = plan.r0 + plan.workers.start(min(wk + 1, NW));
+    Cursor cur = place[min(wk, NW - 1)];
 
     // ------------------------------------------------------- the ring ----
-    // row groups past the last row have nothing to do
-    auto idle_pass = [&](int hp) { return NT == 2 && (hp % a.passes) * kPassRows + rgi * 16 >= a.R; };
+    // row groups past the last row have nothing to do (not with NT = 1: rg * passes groups are full)
+    auto idle_pass = [&](int hp) { return NT == 2 && (hp % a.passes) * a.pass_rows + rgi * C::kRows >= a.R; };
     // lane i copies chunk i % NB of positions i / NB, + 32 / NB, ... of keys and
     // values, then 16 bytes of the scales (one half-warp each)
     constexpr int kPer = 32 / NB;                     // positions per step: a multiple of the swizzle's period
@@ -470,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         const int sb = cur.b, shp = cur.hp, st0 = cur.t, snu = cur.nu;
         const int ue = min(w1, u + snu - st0);
         const int pass = a.passes == 1 ? 0 : shp % a.passes, h = a.passes == 1 ? shp : shp / a.passes;
-        const int row_base = pass * kPassRows + rgi * 16;
+        const int row_base = pass * a.pass_rows + rgi * C::kRows;
         const int L = length(sb);
         const bool idle = idle_pass(shp);
 
@@ -478,7 +493,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         // nibbles); the lane's row is g of each tile.  What follows a score is
         // held for the accumulator's rows, 2 t4 + e.
         uint32_t qf[NT][NB][2][2];
-        float mul[NT][2], koff[NT][NB][4];
+        float mul[NT][2], koff[NT][kSignedK ? 1 : NB][4];
         int lim[NT][2];                               // positions a row sees
         uint2 v[NT][NB][2];
         int tok[NT];
@@ -514,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             const int k = top == 0 || top >= 0x7c00 ? 0 : 28 - max(top >> 10, 1);
             const float f = a.scale2 < 0.0f ? -pow2i(k) : pow2i(k);
             // positive, so that a masked score of -inf stays one
-            const float back = fmaxf(fabsf(a.scale2) * pow2i(24 - k), 1e-37f);
+            const float back = fmaxf(fabsf(a.scale2) * pow2i((kSignedK ? 0 : 24) - k), 1e-37f);
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 mul[r][e] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4 * e);
@@ -522,17 +537,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             }
 #pragma unroll
             for (int j = 0; j < NB; j++) {
-                float (&z)[4] = koff[r][j];
+                float (&z)[4] = koff[r][kSignedK ? 0 : j];
                 z[0] = z[1] = z[2] = z[3] = 0.0f;
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
-                    const float fh = hf ? f * 0.0625f : f;
+                    const float fh = hf && !kSignedK ? f * 0.0625f : f;
                     // register e holds elements 4 t4 + e and 4 t4 + 2 + e: the order of the masked key bytes
                     qf[r][j][hf][0] = pack_f16x2(f16_lo(v[r][j][hf].x) * fh, f16_lo(v[r][j][hf].y) * fh);
                     qf[r][j][hf][1] = pack_f16x2(f16_hi(v[r][j][hf].x) * fh, f16_hi(v[r][j][hf].y) * fh);
-                    // -8 2^-24 (-128 2^-24) as fp16 subnormals
-                    const uint32_t zp = hf ? 0x80808080u : 0x80088008u;
-                    mma(z, zp, zp, zp, zp, qf[r][j][hf][0], qf[r][j][hf][1]);
+                    if constexpr (!kSignedK) {        // -8 2^-24 (-128 2^-24) as fp16 subnormals
+                        const uint32_t zp = hf ? 0x80808080u : 0x80088008u;
+                        mma(z, zp, zp, zp, zp, qf[r][j][hf][0], qf[r][j][hf][1]);
+                    }
                 }
             }
         }
@@ -583,15 +599,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll
                     for (int j = 0; j < NB; j++) {
                         const uint32_t x0 = kx[0][j], x1 = kx[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
+                        const uint32_t l0 = code_lo<kSignedK>(x0), l1 = code_lo<kSignedK>(x1);
+                        const uint32_t l2 = code_lo<kSignedK>(y0), l3 = code_lo<kSignedK>(y1);
+                        const uint32_t h0 = code_hi<kSignedK>(x0), h1 = code_hi<kSignedK>(x1);
+                        const uint32_t h2 = code_hi<kSignedK>(y0), h3 = code_hi<kSignedK>(y1);
                         float c[NT][4];
 #pragma unroll
-                        for (int r = 0; r < NT; r++)
-                            mma_from(c[r], koff[r][j], x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu,
-                                 qf[r][j][0][0], qf[r][j][0][1]);
+                        for (int r = 0; r < NT; r++) {
+                            if constexpr (kSignedK)
+                                mma0(c[r], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
+                            else
+                                mma_from(c[r], koff[r][j], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
+                        }
 #pragma unroll
                         for (int r = 0; r < NT; r++)
-                            mma(c[r], x0 & 0x00F000F0u, x1 & 0x00F000F0u, y0 & 0x00F000F0u, y1 & 0x00F000F0u,
-                                qf[r][j][1][0], qf[r][j][1][1]);
+                            mma(c[r], h0, h1, h2, h3, qf[r][j][1][0], qf[r][j][1][1]);
 #pragma unroll
                         for (int r = 0; r < NT; r++)
 #pragma unroll
@@ -762,11 +784,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     const size_t gp = (size_t)rows_cta * (D + 2);     // floats of a CTA partial
     auto pass_of = [&](const Entry &e) { return a.passes == 1 ? 0 : e.hp % a.passes; };
     auto out_row = [&](const Entry &e, int row) {     // output of a pass's row (row < R checked by the caller)
-        const int rr = pass_of(e) * kPassRows + row, tok = a.Tq == 1 ? 0 : rr / a.G;
+        const int rr = pass_of(e) * a.pass_rows + row, tok = a.Tq == 1 ? 0 : rr / a.G;
         return static_cast<O *>(a.o) + (((size_t)e.b * a.Tq + tok) * a.Hkv * a.G +
                                         (size_t)(a.passes == 1 ? e.hp : e.hp / a.passes) * a.G + (rr - tok * a.G)) * D;
     };
-    auto live_rows = [&](const Entry &e) { return min(rows_cta, a.R - pass_of(e) * kPassRows); };
+    auto live_rows = [&](const Entry &e) { return min(rows_cta, a.R - pass_of(e) * a.pass_rows); };
     // Entries of one segment are consecutive (the invalid ones skipped): a group
     // is worker wa's entry and the first entry of each following worker.
     Entry mine = {-1, 0, 0, 0};
@@ -789,11 +811,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         group[k] = make_int2(lane, (31 - __clz(group_of(lane))) >> 1);
     }
     __syncthreads();
-    constexpr int kItemsLog = (NT == 1 ? 3 : 4) + (D == 128 ? 5 : 4);     // of a row group: kRows * D / 4
-    const int n_groups = __popc(heads), items_log = kItemsLog + rg_log;
+    const int n_groups = __popc(heads);
+    constexpr int kItems = C::kRows * (D / 4);        // of a row group
 #pragma unroll 1
-    for (int it = threadIdx.x; it < n_groups << items_log; it += C::kThreads) {
-        const int k = it >> items_log, row = (it & ((1 << items_log) - 1)) / (D / 4), d = it % (D / 4) * 4;
+    for (int it = threadIdx.x; it < n_groups * a.rg * kItems; it += C::kThreads) {
+        const int kr = it / kItems, k = (kr * a.rg_inv) >> 16;      // row group of a merged segment
+        const int row = (kr - k * a.rg) * C::kRows + it % kItems / (D / 4), d = it % (D / 4) * 4;
         const int i = group[k].x, wb = group[k].y, wa = i >> 1;
         const Entry e = entry[i];
         if (row >= live_rows(e))
@@ -941,8 +964,36 @@ int32_t launch(Args &a, int grid, void *stream)
                : BQ_ERR_CUDA;
 }
 
-// Rows of a CTA partial.
-int part_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : kPassRows; }
+// How R query rows of a KV head are taken: 8 NT rows a warp, rg such groups side
+// by side over the same units (the cache is copied rg times from L2, read once
+// from memory), and passes over the segment.
+struct Shape {
+    int nt, rg, passes;
+    int rows() const { return 8 * nt * rg; }
+};
+// What a pass costs (us at 64 segments of 8192 positions, D = 128, beyond the
+// 12 us that reading them takes): 8-row warps 14, 42 (3 groups, 15 of 16 warps
+// busy), 67 (5 groups); 16-row warps, which unpack codes once for two tiles but
+// run 2 a scheduler instead of 4, 25 and 50 (2 groups).  The least sum is taken.
+// Measured: 40 rows 79 us as 5 groups of 8, 112 as 3 of 16; 48 rows 83 us in two
+// passes of 3 groups of 8, 113 as 3 of 16; 64 rows 104 us in two passes of 2
+// groups of 16, 117 in one of 4.
+Shape shape_of(int R)
+{
+    static const struct { int nt, rg, cost; } kWays[] = {{1, 1, 14}, {2, 1, 25}, {1, 3, 42}, {2, 2, 50}, {1, 5, 67}};
+    Shape best = {2, 2, 0};
+    int least = 1 << 30;
+    for (const auto &w : kWays) {
+        const int group = 8 * w.nt, groups = (R + group - 1) / group, passes = (groups + w.rg - 1) / w.rg;
+        if (w.nt == 1 && groups % w.rg != 0)          // (8-row warps are never idle)
+            continue;
+        if (passes * w.cost < least) {
+            least = passes * w.cost;
+            best = {w.nt, w.rg, passes};
+        }
+    }
+    return best;
+}
 
 }  // namespace aq
 }  // namespace bq
@@ -953,7 +1004,7 @@ extern "C" size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G)
 {
     if ((D != 64 && D != 128) || Tq < 1 || Tq > 32 || G < 1 || G > 16)
         return 0;
-    return aq::kMaxGrid * sizeof(int) + (size_t)aq::kMaxGrid * 2 * aq::part_rows(Tq * G) * (D + 2) * sizeof(float);
+    return aq::kMaxGrid * sizeof(int) + (size_t)aq::kMaxGrid * 2 * aq::shape_of(Tq * G).rows() * (D + 2) * sizeof(float);
 }
 
 extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q, const int32_t *lens,
@@ -972,9 +1023,9 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
         return BQ_ERR_BATCH;
     const long long rows = (long long)B * Hkv < (1LL << 31) ? (long long)B * Hkv * kv->Tmax : 1LL << 31;
     const int R = Tq * G;
-    const int passes = (R + aq::kPassRows - 1) / aq::kPassRows;
+    const aq::Shape shape = aq::shape_of(R);
     // positions, and units of all passes, are 32-bit numbers
-    if (rows >= (1LL << 31) || rows / 32 * passes >= (1LL << 31))
+    if (rows >= (1LL << 31) || rows / 32 * shape.passes >= (1LL << 31))
         return BQ_ERR_SHAPE;
     if (!aligned16(kv->k_codes) || !aligned16(kv->k_scales) || !aligned16(kv->v_codes) ||
         !aligned16(kv->v_scales) || !aligned16(q) || !aligned16(o) || !aligned16(ws) ||
@@ -1001,19 +1052,21 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     a.G = G;
     a.Tmax = kv->Tmax;
     a.R = R;
-    a.rg = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-    a.passes = passes;
+    a.rg = shape.rg;
+    a.rg_inv = 65536 / a.rg + 1;
+    a.passes = shape.passes;
+    a.pass_rows = shape.rows();
     a.scale2 = scale * 1.4426950408889634f;
     a.counters = static_cast<int *>(ws);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + aq::kMaxGrid * sizeof(int));
     const int grid = sms < aq::kMaxGrid ? sms : aq::kMaxGrid;
     const bool f16 = o_dtype == BQ_F16;
     if (kv->D == 128) {
-        if (R <= 8)
+        if (shape.nt == 1)
             return f16 ? aq::launch<128, 1, __half>(a, grid, stream) : aq::launch<128, 1, float>(a, grid, stream);
         return f16 ? aq::launch<128, 2, __half>(a, grid, stream) : aq::launch<128, 2, float>(a, grid, stream);
     }
-    if (R <= 8)
+    if (shape.nt == 1)
         return f16 ? aq::launch<64, 1, __half>(a, grid, stream) : aq::launch<64, 1, float>(a, grid, stream);
     return f16 ? aq::launch<64, 2, __half>(a, grid, stream) : aq::launch<64, 2, float>(a, grid, stream);
 }

@@ -34,10 +34,19 @@ CASES = [
     (1, 32, 1, 16, 128, 128, [100]),
     (2, 32, 2, 1, 64, 64, [40, 20]),
     (1, 7, 1, 11, 128, 9600, [9533]),
+    (2, 8, 2, 6, 128, 2048, [2048, 33]),
+    (1, 7, 2, 8, 64, 1024, [1023]),
+    (2, 9, 1, 8, 128, 512, [500, 8]),
+    (3, 3, 3, 8, 128, 800, [800, 33, 790]),
     (40, 1, 2, 2, 128, 64, [(7 * i) % 65 for i in range(40)]),
     (300, 1, 2, 1, 64, 32, [(5 * i) % 33 for i in range(300)]),
     (2, 1, 1, 4, 128, 32768, [32768, 5]),
     (6, 1, 4, 3, 128, 2048, [2048, 0, 1, 1999, 0, 640]),
+    # shares: segments with CTAs of their own, short ones that are not cut, long and short mixed
+    (9, 1, 2, 4, 128, 8192, [8192, 8191, 4097, 33, 8000, 7777, 6000, 1, 8192]),
+    (100, 1, 3, 2, 64, 1024, [(37 * i) % 1025 for i in range(100)]),
+    (70, 1, 1, 5, 128, 4096, [4096 if i % 9 == 4 else (11 * i) % 200 for i in range(70)]),
+    (33, 2, 4, 3, 128, 1056, [1056 - i for i in range(33)]),
 ]
 
 
