@@ -9,7 +9,7 @@
 // Work: a unit is 32 positions of one (sequence, KV head).  The valid units of
 // all sequences form one line (lens are on the device, so every warp builds the
 // prefix sums itself); CTAs take equal consecutive shares of it, and a CTA's
-// workers (warps) equal consecutive shares of the CTA's.  Ragged lengths
+// warps equal consecutive shares of the CTA's.  Ragged lengths
 // therefore cost no balance, and a sequence that ends inside a share just
 // starts the next one: a warp never waits for another before its line ends.
 // A warp streams its units through a ring of its own in shared memory with
@@ -60,7 +60,7 @@ constexpr int kSnap = 32;                 // segments up to this length are neve
 constexpr float kFloor = -3.0e38f;        // a reference no score has reached
 constexpr float kBase = 11.0f, kSlack = 4.0f;
 
-// D: head width; NT: 8-row tiles per warp (1 or 2: see shape_of).
+// D: head width; NT: 8-row tiles per warp (1 or 2: see tiles_of).
 template <int D, int NT>
 struct Cfg {
     static constexpr int kNB = D / 32;                        // blocks per row
@@ -90,8 +90,7 @@ struct Args {
     void *o;
     int B, Tq, Hkv, G, Tmax;
     int R;                                // Tq * G query rows per KV head
-    int rg, passes, pass_rows;            // row groups (of 8 NT rows) a CTA takes at once, passes of pass_rows = 8 NT rg rows
-    int rg_inv;                           // warp / rg = warp * rg_inv >> 16
+    int passes;                           // of 8 NT rows each
     float scale2;                         // scale * log2(e)
     int *counters;                        // [grid], by a shared segment's first CTA
     float *partials;                      // [grid][2]: O [rows][D], then (m, l) [rows]
@@ -255,7 +254,7 @@ struct Plan {
     int n_act;                            // CTAs with work
     int split;                            // 1: the CTA's segment has CTAs of its own, cf .. cl
     int r0, r1, cf, cl;                   // its units (split: counted from the segment's start)
-    Shares line, workers;                 // even shares of the line and of r0 .. r1
+    Shares line, warps;                   // even shares of the line and of r0 .. r1
 };
 
 template <int D, int NT, typename O>
@@ -268,11 +267,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     // points would take 32 registers.
     constexpr bool kSignedK = NT == 2;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Entry entry[2 * W];                    // worker w: 2w (began before its share), 2w + 1
+    __shared__ Entry entry[2 * W];                    // warp w: 2w (began before its share), 2w + 1
     __shared__ int arrived[2];
     __shared__ Plan plan;
-    __shared__ Cursor place[W], copy_at[W];           // workers' starts; what each warp copies next
-    __shared__ int2 group[2 * W];                     // first entry, last worker of each merged segment
+    __shared__ Cursor place[W], copy_at[W];           // warps' starts; what each copies next
+    __shared__ int2 group[2 * W];                     // first entry, last warp of each merged segment
 
     uint8_t *sbase = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -281,8 +280,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     float *const last_part = reinterpret_cast<float *>(mine_raw);
     float *const first_part = reinterpret_cast<float *>(sbase + W * C::kWarpBytes) + warp * C::kPart;
     const int HP = a.Hkv * a.passes, cta = blockIdx.x;
-    // workers: rg warps each, one per row group
-    const int NW = (W * a.rg_inv) >> 16, wk = (warp * a.rg_inv) >> 16, rgi = warp - wk * a.rg;
 
     if (threadIdx.x < W * 2)
         entry[threadIdx.x].b = -1;
@@ -399,15 +396,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 pl.r0 = __shfl_sync(0xffffffffu, x, 0), pl.r1 = __shfl_sync(0xffffffffu, x, 1);
                 pl.cf = pl.cl = 0;
             }
-            // (workers without units, if any, are the CTA's last: the merge counts on it)
-            const int each = (pl.r1 - pl.r0) / NW;
-            pl.workers = {each, pl.r1 - pl.r0 - each * NW};
-            const int w0 = pl.r0 + pl.workers.start(min(lane, NW));
+            // (warps without units, if any, are the CTA's last: the merge counts on it)
+            pl.warps = {(pl.r1 - pl.r0) / W, (pl.r1 - pl.r0) % W};
+            const int w0 = pl.r0 + pl.warps.start(min(lane, W));
             if (split)
                 c.t = w0;
             else
                 c = locate(min(w0, U - 1));
-            if (lane < NW)
+            if (lane < W)
                 place[lane] = c;
         }
         if (lane == 0)
@@ -432,12 +428,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             c.nu = c.b < a.B ? units_of(c.b) : 1;
         } while (c.nu == 0);
     };
-    const int w0 = plan.r0 + plan.workers.start(min(wk, NW)), w1 = plan.r0 + plan.workers.start(min(wk + 1, NW));
-    Cursor cur = place[min(wk, NW - 1)];
+    const int w0 = plan.r0 + plan.warps.start(warp), w1 = plan.r0 + plan.warps.start(warp + 1);
+    Cursor cur = place[warp];
 
     // ------------------------------------------------------- the ring ----
-    // row groups past the last row have nothing to do (not with NT = 1: rg * passes groups are full)
-    auto idle_pass = [&](int hp) { return NT == 2 && (hp % a.passes) * a.pass_rows + rgi * C::kRows >= a.R; };
     // lane i copies chunk i % NB of positions i / NB, + 32 / NB, ... of keys and
     // values, then 16 bytes of the scales (one half-warp each)
     constexpr int kPer = 32 / NB;                     // positions per step: a multiple of the swizzle's period
@@ -485,9 +479,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         const int sb = cur.b, shp = cur.hp, st0 = cur.t, snu = cur.nu;
         const int ue = min(w1, u + snu - st0);
         const int pass = a.passes == 1 ? 0 : shp % a.passes, h = a.passes == 1 ? shp : shp / a.passes;
-        const int row_base = pass * a.pass_rows + rgi * C::kRows;
+        const int row_base = pass * C::kRows;
         const int L = length(sb);
-        const bool idle = idle_pass(shp);
 
         // query fragments (B of the score product): block j, half hf (low / high
         // nibbles); the lane's row is g of each tile.  What follows a score is
@@ -567,148 +560,146 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
             __syncwarp();                             // every lane's copies of this unit have landed
             const uint32_t vb = kb + C::kCodes;
-            if (!idle) {
-                // ------------------------------------------ scales ----
-                // lane i converts position i's; past the length the cache may
-                // hold anything: scales of 0
-                const bool valid = t0 + lane < L;
-                (void)convert_scales<NB>(conv + lane * NB * 4, kb + 2 * C::kCodes + lane * NB * 2, valid);
-                const uint32_t vmax = __reduce_max_sync(
-                    0xffffffffu, convert_scales<NB>(conv + (kUnit + lane) * NB * 4, kb + 2 * C::kCodes + C::kScales + lane * NB * 2, valid));
-                __syncwarp();
-                // ------------------------------------------ scores ----
-                // s[r][p][e]: row 2 t4 + e of tile r, position 8 p + g
-                float s[NT][4][2];
+            // ------------------------------------------ scales ----
+            // lane i converts position i's; past the length the cache may
+            // hold anything: scales of 0
+            const bool valid = t0 + lane < L;
+            (void)convert_scales<NB>(conv + lane * NB * 4, kb + 2 * C::kCodes + lane * NB * 2, valid);
+            const uint32_t vmax = __reduce_max_sync(
+                0xffffffffu, convert_scales<NB>(conv + (kUnit + lane) * NB * 4, kb + 2 * C::kCodes + C::kScales + lane * NB * 2, valid));
+            __syncwarp();
+            // ------------------------------------------ scores ----
+            // s[r][p][e]: row 2 t4 + e of tile r, position 8 p + g
+            float s[NT][4][2];
 #pragma unroll
-                for (int mt = 0; mt < 2; mt++) {      // 16 positions
-                    uint32_t kx[2][NB];
-                    if constexpr (D == 128) {
+            for (int mt = 0; mt < 2; mt++) {      // 16 positions
+                uint32_t kx[2][NB];
+                if constexpr (D == 128) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        ldsm4(kx[i], kb + swizzled<D>(16 * mt + 8 * i + (lane & 7), lane >> 3));
+                } else {
+                    uint32_t t[4];                // positions 0-7: blocks 0, 1; positions 8-15: blocks 0, 1
+                    ldsm4(t, kb + swizzled<D>(16 * mt + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
+                    kx[0][0] = t[0], kx[0][1] = t[1], kx[1][0] = t[2], kx[1][1] = t[3];
+                }
+                float dk[2][NB];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    row_scales<NB>(dk[i], conv + (16 * mt + 8 * i + g) * NB * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < NB; j++) {
+                    const uint32_t x0 = kx[0][j], x1 = kx[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
+                    const uint32_t l0 = code_lo<kSignedK>(x0), l1 = code_lo<kSignedK>(x1);
+                    const uint32_t l2 = code_lo<kSignedK>(y0), l3 = code_lo<kSignedK>(y1);
+                    const uint32_t h0 = code_hi<kSignedK>(x0), h1 = code_hi<kSignedK>(x1);
+                    const uint32_t h2 = code_hi<kSignedK>(y0), h3 = code_hi<kSignedK>(y1);
+                    float c[NT][4];
+#pragma unroll
+                    for (int r = 0; r < NT; r++) {
+                        if constexpr (kSignedK)
+                            mma0(c[r], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
+                        else
+                            mma_from(c[r], koff[r][j], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < NT; r++)
+                        mma(c[r], h0, h1, h2, h3, qf[r][j][1][0], qf[r][j][1][1]);
+#pragma unroll
+                    for (int r = 0; r < NT; r++)
 #pragma unroll
                         for (int i = 0; i < 2; i++)
-                            ldsm4(kx[i], kb + swizzled<D>(16 * mt + 8 * i + (lane & 7), lane >> 3));
-                    } else {
-                        uint32_t t[4];                // positions 0-7: blocks 0, 1; positions 8-15: blocks 0, 1
-                        ldsm4(t, kb + swizzled<D>(16 * mt + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1));
-                        kx[0][0] = t[0], kx[0][1] = t[1], kx[1][0] = t[2], kx[1][1] = t[3];
-                    }
-                    float dk[2][NB];
-#pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        row_scales<NB>(dk[i], conv + (16 * mt + 8 * i + g) * NB * 4);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NB; j++) {
-                        const uint32_t x0 = kx[0][j], x1 = kx[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
-                        const uint32_t l0 = code_lo<kSignedK>(x0), l1 = code_lo<kSignedK>(x1);
-                        const uint32_t l2 = code_lo<kSignedK>(y0), l3 = code_lo<kSignedK>(y1);
-                        const uint32_t h0 = code_hi<kSignedK>(x0), h1 = code_hi<kSignedK>(x1);
-                        const uint32_t h2 = code_hi<kSignedK>(y0), h3 = code_hi<kSignedK>(y1);
-                        float c[NT][4];
-#pragma unroll
-                        for (int r = 0; r < NT; r++) {
-                            if constexpr (kSignedK)
-                                mma0(c[r], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
-                            else
-                                mma_from(c[r], koff[r][j], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
-                        }
-#pragma unroll
-                        for (int r = 0; r < NT; r++)
-                            mma(c[r], h0, h1, h2, h3, qf[r][j][1][0], qf[r][j][1][1]);
-#pragma unroll
-                        for (int r = 0; r < NT; r++)
-#pragma unroll
-                            for (int i = 0; i < 2; i++)
-#pragma unroll
-                                for (int e = 0; e < 2; e++)
-                                    s[r][2 * mt + i][e] = j == 0 ? dk[i][0] * c[r][2 * i + e]
-                                                                 : fmaf(dk[i][j], c[r][2 * i + e], s[r][2 * mt + i][e]);
-                    }
-                }
-                if (t0 + kUnit > L - (a.Tq - 1)) {    // some row's positions end in this unit
-#pragma unroll
-                    for (int p = 0; p < 4; p++)
-#pragma unroll
-                        for (int r = 0; r < NT; r++)
 #pragma unroll
                             for (int e = 0; e < 2; e++)
-                                s[r][p][e] = t0 + 8 * p + g < lim[r][e] ? s[r][p][e] : -INFINITY;
+                                s[r][2 * mt + i][e] = j == 0 ? dk[i][0] * c[r][2 * i + e]
+                                                             : fmaf(dk[i][j], c[r][2 * i + e], s[r][2 * mt + i][e]);
                 }
-                // --------------------------------- running reference ----
-                // the unit's bound on log2(dV), and per row on s + log2(dV) - kBase
-                const float eb = fmaf((float)vmax, 0x1p-10f, -15.0f - kBase);
-                bool grow = false;
-                float cand[NT][2];
+            }
+            if (t0 + kUnit > L - (a.Tq - 1)) {    // some row's positions end in this unit
+#pragma unroll
+                for (int p = 0; p < 4; p++)
+#pragma unroll
+                    for (int r = 0; r < NT; r++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+                            s[r][p][e] = t0 + 8 * p + g < lim[r][e] ? s[r][p][e] : -INFINITY;
+            }
+            // --------------------------------- running reference ----
+            // the unit's bound on log2(dV), and per row on s + log2(dV) - kBase
+            const float eb = fmaf((float)vmax, 0x1p-10f, -15.0f - kBase);
+            bool grow = false;
+            float cand[NT][2];
+#pragma unroll
+            for (int r = 0; r < NT; r++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float mx = fmaxf(fmaxf(s[r][0][e], s[r][1][e]), fmaxf(s[r][2][e], s[r][3][e]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    cand[r][e] = __fmaf_ru(mx, mul[r][e], eb);   // (rounded up: scores of any size keep p dV in range)
+                    grow = grow || cand[r][e] - m[r][e] > kSlack;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int r = 0; r < NT; r++)
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
-                        float mx = fmaxf(fmaxf(s[r][0][e], s[r][1][e]), fmaxf(s[r][2][e], s[r][3][e]));
+                        const float mn = fmaxf(m[r][e], cand[r][e]), f = ex2(m[r][e] - mn);
+                        m[r][e] = mn;
+                        l[r][e] *= f;
 #pragma unroll
-                        for (int off = 4; off < 32; off <<= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                        cand[r][e] = __fmaf_ru(mx, mul[r][e], eb);   // (rounded up: scores of any size keep p dV in range)
-                        grow = grow || cand[r][e] - m[r][e] > kSlack;
+                        for (int i = 0; i < 2 * NB; i++) {
+                            acc[r][i][e] *= f;
+                            acc[r][i][e + 2] *= f;
+                        }
                     }
-                if (__any_sync(0xffffffffu, grow)) {
+            }
 #pragma unroll
-                    for (int r = 0; r < NT; r++)
+            for (int r = 0; r < NT; r++)
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const float mn = fmaxf(m[r][e], cand[r][e]), f = ex2(m[r][e] - mn);
-                            m[r][e] = mn;
-                            l[r][e] *= f;
+                for (int p = 0; p < 4; p++)
 #pragma unroll
-                            for (int i = 0; i < 2 * NB; i++) {
-                                acc[r][i][e] *= f;
-                                acc[r][i][e + 2] *= f;
+                    for (int e = 0; e < 2; e++) {
+                        float &w = s[r][p][e];
+                        w = ex2(fmaf(w, mul[r][e], -m[r][e]));
+                        l[r][e] += w;
+                    }
+            // ------------------------------------------ values ----
+#pragma unroll
+            for (int k = 0; k < 2; k++) {         // 16 positions
+                float dv[2][NB];
+                row_scales<NB>(dv[0], conv + (kUnit + 16 * k + g) * NB * 4);
+                row_scales<NB>(dv[1], conv + (kUnit + 16 * k + 8 + g) * NB * 4);
+#pragma unroll
+                for (int j2 = 0; j2 < NB / 2; j2++) {
+                    uint32_t x[4];                // block 2 j2: positions 0-7, 8-15; block 2 j2 + 1
+                    ldsm4t(x, vb + swizzled<D>(16 * k + (lane & 15), 2 * j2 + (lane >> 4)));
+#pragma unroll
+                    for (int jj = 0; jj < 2; jj++) {
+                        const int j = 2 * j2 + jj;
+                        uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+                        for (int r = 0; r < NT; r++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {
+                                const float p0 = s[r][2 * k + i][0] * dv[i][j], p1 = s[r][2 * k + i][1] * dv[i][j];
+                                const uint32_t w = pack_f16x2(p0, p1);
+                                bh[r][i] = transposed(w);
+                                if constexpr (kTwo)
+                                    bl[r][i] = transposed(pack_f16x2(p0 - f16_lo(w), p1 - f16_hi(w)));
                             }
-                        }
-                }
+                        const uint32_t x0 = x[2 * jj], x1 = x[2 * jj + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+                        const uint32_t e0 = nib_lo(x0), e1 = nib_hi(x0), e2 = nib_lo(x1), e3 = nib_hi(x1);
+                        const uint32_t f0 = nib_lo(y0), f1 = nib_hi(y0), f2 = nib_lo(y1), f3 = nib_hi(y1);
 #pragma unroll
-                for (int r = 0; r < NT; r++)
-#pragma unroll
-                    for (int p = 0; p < 4; p++)
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            float &w = s[r][p][e];
-                            w = ex2(fmaf(w, mul[r][e], -m[r][e]));
-                            l[r][e] += w;
-                        }
-                // ------------------------------------------ values ----
-#pragma unroll
-                for (int k = 0; k < 2; k++) {         // 16 positions
-                    float dv[2][NB];
-                    row_scales<NB>(dv[0], conv + (kUnit + 16 * k + g) * NB * 4);
-                    row_scales<NB>(dv[1], conv + (kUnit + 16 * k + 8 + g) * NB * 4);
-#pragma unroll
-                    for (int j2 = 0; j2 < NB / 2; j2++) {
-                        uint32_t x[4];                // block 2 j2: positions 0-7, 8-15; block 2 j2 + 1
-                        ldsm4t(x, vb + swizzled<D>(16 * k + (lane & 15), 2 * j2 + (lane >> 4)));
-#pragma unroll
-                        for (int jj = 0; jj < 2; jj++) {
-                            const int j = 2 * j2 + jj;
-                            uint32_t bh[NT][2], bl[NT][2];
-#pragma unroll
-                            for (int r = 0; r < NT; r++)
-#pragma unroll
-                                for (int i = 0; i < 2; i++) {
-                                    const float p0 = s[r][2 * k + i][0] * dv[i][j], p1 = s[r][2 * k + i][1] * dv[i][j];
-                                    const uint32_t w = pack_f16x2(p0, p1);
-                                    bh[r][i] = transposed(w);
-                                    if constexpr (kTwo)
-                                        bl[r][i] = transposed(pack_f16x2(p0 - f16_lo(w), p1 - f16_hi(w)));
-                                }
-                            const uint32_t x0 = x[2 * jj], x1 = x[2 * jj + 1], y0 = x0 >> 8, y1 = x1 >> 8;
-                            const uint32_t e0 = nib_lo(x0), e1 = nib_hi(x0), e2 = nib_lo(x1), e3 = nib_hi(x1);
-                            const uint32_t f0 = nib_lo(y0), f1 = nib_hi(y0), f2 = nib_lo(y1), f3 = nib_hi(y1);
-#pragma unroll
-                            for (int r = 0; r < NT; r++) {
-                                mma(acc[r][2 * j], e0, e1, e2, e3, bh[r][0], bh[r][1]);
-                                mma(acc[r][2 * j + 1], f0, f1, f2, f3, bh[r][0], bh[r][1]);
-                                if constexpr (kTwo) {
-                                    mma(acc[r][2 * j], e0, e1, e2, e3, bl[r][0], bl[r][1]);
-                                    mma(acc[r][2 * j + 1], f0, f1, f2, f3, bl[r][0], bl[r][1]);
-                                }
+                        for (int r = 0; r < NT; r++) {
+                            mma(acc[r][2 * j], e0, e1, e2, e3, bh[r][0], bh[r][1]);
+                            mma(acc[r][2 * j + 1], f0, f1, f2, f3, bh[r][0], bh[r][1]);
+                            if constexpr (kTwo) {
+                                mma(acc[r][2 * j], e0, e1, e2, e3, bl[r][0], bl[r][1]);
+                                mma(acc[r][2 * j + 1], f0, f1, f2, f3, bl[r][0], bl[r][1]);
                             }
                         }
                     }
@@ -730,21 +721,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                     l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], off);
         const bool before = st0 > 0, after = t0 < snu * kUnit;
         if (!before && !after) {
-            if (!idle) {
 #pragma unroll
-                for (int r = 0; r < NT; r++) {
+            for (int r = 0; r < NT; r++) {
 #pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        const float fi = l[r][c] > 0.0f ? 1.0f / l[r][c] : 0.0f;
-                        const int row = row_base + 8 * r + 2 * t4 + c;
-                        if (row < a.R) {
-                            O *o = static_cast<O *>(a.o) +
-                                   (((size_t)sb * a.Tq + row / a.G) * a.Hkv * a.G + (size_t)h * a.G + row % a.G) * D;
+                for (int c = 0; c < 2; c++) {
+                    const float fi = l[r][c] > 0.0f ? 1.0f / l[r][c] : 0.0f;
+                    const int row = row_base + 8 * r + 2 * t4 + c;
+                    if (row < a.R) {
+                        O *o = static_cast<O *>(a.o) +
+                               (((size_t)sb * a.Tq + row / a.G) * a.Hkv * a.G + (size_t)h * a.G + row % a.G) * D;
 #pragma unroll
-                            for (int j = 0; j < NB; j++) {
-                                store2(o + 32 * j + 2 * g, acc[r][2 * j][c] * fi, acc[r][2 * j + 1][c] * fi);
-                                store2(o + 32 * j + 16 + 2 * g, acc[r][2 * j][c + 2] * fi, acc[r][2 * j + 1][c + 2] * fi);
-                            }
+                        for (int j = 0; j < NB; j++) {
+                            store2(o + 32 * j + 2 * g, acc[r][2 * j][c] * fi, acc[r][2 * j + 1][c] * fi);
+                            store2(o + 32 * j + 16 + 2 * g, acc[r][2 * j][c + 2] * fi, acc[r][2 * j + 1][c + 2] * fi);
                         }
                     }
                 }
@@ -754,8 +743,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             // slot; one that only continues after it is the share's last, and
             // the ring is drained
             float *pp = before ? first_part : last_part;
-            if (lane == 0 && rgi == 0)
-                entry[2 * wk + (before ? 0 : 1)] = {sb, shp, u - t0 / kUnit, snu};
+            if (lane == 0)
+                entry[2 * warp + (before ? 0 : 1)] = {sb, shp, u - t0 / kUnit, snu};
 #pragma unroll
             for (int r = 0; r < NT; r++) {
 #pragma unroll
@@ -779,20 +768,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     }
     __syncthreads();
 
-    // ------------------------------------------------ merge the workers ----
-    const int rows_cta = C::kRows * a.rg;             // rows of a pass
-    const size_t gp = (size_t)rows_cta * (D + 2);     // floats of a CTA partial
+    // ------------------------------------------------ merge the warps ----
+    constexpr size_t gp = (size_t)C::kRows * (D + 2); // floats of a CTA partial
     auto pass_of = [&](const Entry &e) { return a.passes == 1 ? 0 : e.hp % a.passes; };
     auto out_row = [&](const Entry &e, int row) {     // output of a pass's row (row < R checked by the caller)
-        const int rr = pass_of(e) * a.pass_rows + row, tok = a.Tq == 1 ? 0 : rr / a.G;
+        const int rr = pass_of(e) * C::kRows + row, tok = a.Tq == 1 ? 0 : rr / a.G;
         return static_cast<O *>(a.o) + (((size_t)e.b * a.Tq + tok) * a.Hkv * a.G +
                                         (size_t)(a.passes == 1 ? e.hp : e.hp / a.passes) * a.G + (rr - tok * a.G)) * D;
     };
-    auto live_rows = [&](const Entry &e) { return min(rows_cta, a.R - pass_of(e) * a.pass_rows); };
+    auto live_rows = [&](const Entry &e) { return min(C::kRows, a.R - pass_of(e) * C::kRows); };
     // Entries of one segment are consecutive (the invalid ones skipped): a group
-    // is worker wa's entry and the first entry of each following worker.
+    // is warp wa's entry and the first entry of each following warp.
     Entry mine = {-1, 0, 0, 0};
-    if (lane < 2 * NW)
+    if (lane < 2 * W)
         mine = entry[lane];
     const unsigned valid = __ballot_sync(0xffffffffu, mine.b >= 0);
     const unsigned earlier = valid & ((1u << lane) - 1u);
@@ -802,8 +790,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         const unsigned after = heads & ~((2u << i) - 1u);
         return valid & ~((1u << i) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : ~0u);
     };
-    auto entry_part = [&](int k, int rq) -> const float * {
-        const int w = (k >> 1) * a.rg + rq;
+    auto entry_part = [&](int k) {
+        const int w = k >> 1;
         return reinterpret_cast<const float *>(sbase + ((k & 1) ? w * C::kWarpBytes : W * C::kWarpBytes + w * C::kPart * 4));
     };
     if (warp == 0 && (heads >> lane & 1)) {
@@ -812,20 +800,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     }
     __syncthreads();
     const int n_groups = __popc(heads);
-    constexpr int kItems = C::kRows * (D / 4);        // of a row group
+    constexpr int kItems = C::kRows * (D / 4);
 #pragma unroll 1
-    for (int it = threadIdx.x; it < n_groups * a.rg * kItems; it += C::kThreads) {
-        const int kr = it / kItems, k = (kr * a.rg_inv) >> 16;      // row group of a merged segment
-        const int row = (kr - k * a.rg) * C::kRows + it % kItems / (D / 4), d = it % (D / 4) * 4;
+    for (int it = threadIdx.x; it < n_groups * kItems; it += C::kThreads) {
+        const int k = it / kItems, row = it % kItems / (D / 4), d = it % (D / 4) * 4;
         const int i = group[k].x, wb = group[k].y, wa = i >> 1;
         const Entry e = entry[i];
         if (row >= live_rows(e))
             continue;
-        const int rq = row / C::kRows, rr = row % C::kRows;
-        const float *pa = entry_part(i, rq);
-        // worker wa's entry, then the first entries of wa + 1 .. wb
-        const float *pf = entry_part(0, rq);
-        const int step = a.rg * C::kPart, ml = C::kRows * C::kLd + 2 * rr;
+        // warp wa's entry, then the first entries of wa + 1 .. wb
+        const float *pa = entry_part(i), *pf = entry_part(0);
+        constexpr int step = C::kPart;
+        const int ml = C::kRows * C::kLd + 2 * row;
         float M = pa[ml];
 #pragma unroll 8
         for (int w = wa + 1; w <= wb; w++)
@@ -836,7 +822,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         for (int w = wa; w <= wb; w++) {
             const float *pp = w == wa ? pa : pf + w * step;
             const float2 s2 = *reinterpret_cast<const float2 *>(pp + ml);
-            const float4 v = *reinterpret_cast<const float4 *>(pp + rr * C::kLd + d);
+            const float4 v = *reinterpret_cast<const float4 *>(pp + row * C::kLd + d);
             const float f = ex2(s2.x - M);
             L = fmaf(f, s2.y, L);
             o.x = fmaf(f, v.x, o.x);
@@ -850,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             float *gpart = a.partials + ((size_t)cta * 2 + (e.first < plan.r0 ? 0 : 1)) * gp;
             __stcg(reinterpret_cast<float4 *>(gpart + (size_t)row * D + d), o);
             if (d == 0)
-                __stcg(reinterpret_cast<float2 *>(gpart + (size_t)rows_cta * D) + row, make_float2(M, L));
+                __stcg(reinterpret_cast<float2 *>(gpart + (size_t)C::kRows * D) + row, make_float2(M, L));
         }
     }
     // segments other CTAs share: the first and the last group may be
@@ -901,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 for (int i = lane; i < n4; i += 32)
                     copy16(smem_u32(so + (p * n4 + i) * 4), src + (size_t)row0 * D + i * 4);
                 if (2 * lane < nr)
-                    copy16(smem_u32(sml + p * nr2 + 2 * lane), src + (size_t)rows_cta * D + (row0 + 2 * lane) * 2);
+                    copy16(smem_u32(sml + p * nr2 + 2 * lane), src + (size_t)C::kRows * D + (row0 + 2 * lane) * 2);
             }
             asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
             __syncthreads();
@@ -933,7 +919,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 for (int i = lane; i < n4; i += 32)
                     __stcg(reinterpret_cast<float4 *>(src + (size_t)row0 * D) + i, make_float4(0.f, 0.f, 0.f, 0.f));
                 if (2 * lane < nr)
-                    __stcg(reinterpret_cast<float4 *>(src + (size_t)rows_cta * D + row0 * 2) + lane, make_float4(0.f, 0.f, 0.f, 0.f));
+                    __stcg(reinterpret_cast<float4 *>(src + (size_t)C::kRows * D + row0 * 2) + lane, make_float4(0.f, 0.f, 0.f, 0.f));
             }
             __syncthreads();                          // (the space is free again)
         }
@@ -964,35 +950,19 @@ int32_t launch(Args &a, int grid, void *stream)
                : BQ_ERR_CUDA;
 }
 
-// How R query rows of a KV head are taken: 8 NT rows a warp, rg such groups side
-// by side over the same units (the cache is copied rg times from L2, read once
-// from memory), and passes over the segment.
-struct Shape {
-    int nt, rg, passes;
-    int rows() const { return 8 * nt * rg; }
-};
-// What a pass costs (us at 64 segments of 8192 positions, D = 128, beyond the
-// 12 us that reading them takes): 8-row warps 14, 42 (3 groups, 15 of 16 warps
-// busy), 67 (5 groups); 16-row warps, which unpack codes once for two tiles but
-// run 2 a scheduler instead of 4, 25 and 50 (2 groups).  The least sum is taken.
-// Measured: 40 rows 79 us as 5 groups of 8, 112 as 3 of 16; 48 rows 83 us in two
-// passes of 3 groups of 8, 113 as 3 of 16; 64 rows 104 us in two passes of 2
-// groups of 16, 117 in one of 4.
-Shape shape_of(int R)
+// 8-row tiles a warp takes of R query rows, in ceil(R / 8 tiles) passes over a
+// segment.  At 64 segments of 8192 positions (D = 128) a further pass takes 12.4
+// us with one tile; with two, which unpack codes once for both but run 2 warps a
+// scheduler instead of 4, 21.5.  So 24 rows take 55 us in three passes and 61 in
+// two, 40 rows 79 and 82, but 16 rows 42 and 37, 48 rows 92 and 84, and from 7
+// tiles on two a pass are no slower.  (Tiles side by side in a CTA, over one copy
+// of the cache in L2 or shared memory, were no faster: 60 and 64 us at 24 and 32
+// rows, 93 at 40; at 302 MB of cache, past L2, 180, 190 and 286 against 165, 185
+// and 263.)
+int tiles_of(int R)
 {
-    static const struct { int nt, rg, cost; } kWays[] = {{1, 1, 14}, {2, 1, 25}, {1, 3, 42}, {2, 2, 50}, {1, 5, 67}};
-    Shape best = {2, 2, 0};
-    int least = 1 << 30;
-    for (const auto &w : kWays) {
-        const int group = 8 * w.nt, groups = (R + group - 1) / group, passes = (groups + w.rg - 1) / w.rg;
-        if (w.nt == 1 && groups % w.rg != 0)          // (8-row warps are never idle)
-            continue;
-        if (passes * w.cost < least) {
-            least = passes * w.cost;
-            best = {w.nt, w.rg, passes};
-        }
-    }
-    return best;
+    const int t = (R + 7) / 8;
+    return 173 * ((t + 1) / 2) < 100 * t ? 2 : 1;
 }
 
 }  // namespace aq
@@ -1004,7 +974,7 @@ extern "C" size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G)
 {
     if ((D != 64 && D != 128) || Tq < 1 || Tq > 32 || G < 1 || G > 16)
         return 0;
-    return aq::kMaxGrid * sizeof(int) + (size_t)aq::kMaxGrid * 2 * aq::shape_of(Tq * G).rows() * (D + 2) * sizeof(float);
+    return aq::kMaxGrid * sizeof(int) + (size_t)aq::kMaxGrid * 2 * 8 * aq::tiles_of(Tq * G) * (D + 2) * sizeof(float);
 }
 
 extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q, const int32_t *lens,
@@ -1023,9 +993,9 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
         return BQ_ERR_BATCH;
     const long long rows = (long long)B * Hkv < (1LL << 31) ? (long long)B * Hkv * kv->Tmax : 1LL << 31;
     const int R = Tq * G;
-    const aq::Shape shape = aq::shape_of(R);
+    const int tiles = aq::tiles_of(R), passes = (R + 8 * tiles - 1) / (8 * tiles);
     // positions, and units of all passes, are 32-bit numbers
-    if (rows >= (1LL << 31) || rows / 32 * shape.passes >= (1LL << 31))
+    if (rows >= (1LL << 31) || rows / 32 * passes >= (1LL << 31))
         return BQ_ERR_SHAPE;
     if (!aligned16(kv->k_codes) || !aligned16(kv->k_scales) || !aligned16(kv->v_codes) ||
         !aligned16(kv->v_scales) || !aligned16(q) || !aligned16(o) || !aligned16(ws) ||
@@ -1052,21 +1022,18 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     a.G = G;
     a.Tmax = kv->Tmax;
     a.R = R;
-    a.rg = shape.rg;
-    a.rg_inv = 65536 / a.rg + 1;
-    a.passes = shape.passes;
-    a.pass_rows = shape.rows();
+    a.passes = passes;
     a.scale2 = scale * 1.4426950408889634f;
     a.counters = static_cast<int *>(ws);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + aq::kMaxGrid * sizeof(int));
     const int grid = sms < aq::kMaxGrid ? sms : aq::kMaxGrid;
     const bool f16 = o_dtype == BQ_F16;
     if (kv->D == 128) {
-        if (shape.nt == 1)
+        if (tiles == 1)
             return f16 ? aq::launch<128, 1, __half>(a, grid, stream) : aq::launch<128, 1, float>(a, grid, stream);
         return f16 ? aq::launch<128, 2, __half>(a, grid, stream) : aq::launch<128, 2, float>(a, grid, stream);
     }
-    if (shape.nt == 1)
+    if (tiles == 1)
         return f16 ? aq::launch<64, 1, __half>(a, grid, stream) : aq::launch<64, 1, float>(a, grid, stream);
     return f16 ? aq::launch<64, 2, __half>(a, grid, stream) : aq::launch<64, 2, float>(a, grid, stream);
 }
