@@ -257,6 +257,143 @@ struct Plan {
     Shares line, warps;                   // even shares of the line and of r0 .. r1
 };
 
+__device__ __forceinline__ int length_of(const Args &a, int b) { return min(max(a.lens[b], 0), a.Tmax); }
+__device__ __forceinline__ int units_in(const Args &a, int b) { return (length_of(a, b) + kUnit - 1) / kUnit; }
+
+// ---------------------------------- how the CTAs share the units ----
+// Split: every segment has CTAs of its own, about units / T of them, if that
+// takes no more than the grid with T at most 24 units (3/16) above an even
+// share.  Otherwise the line is cut evenly, and a CTA that shares two segments
+// merges twice, 3 us more, the time of 24 units: 16.5 against 13.5 us at 8
+// segments of 256 units; but 68 us cut evenly against 73 at 64 segments of
+// 1024 units, where T would be 69 more.  A cut inside a short segment moves to
+// its nearer end: 16 units more at most, against a merge across CTAs.
+//
+// Up to 32 sequences a lane has one and the plan is straight-line code on
+// registers; beyond, a lane has a chunk of them, and loops over it (MANY).
+// What this costs is fetching instructions that run once: 4.7 us with loops
+// and integer divisions throughout, 1.5 us so.
+template <bool MANY, int W>
+__device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *place)
+{
+    const int lane = threadIdx.x & 31, cta = blockIdx.x, HP = a.Hkv * a.passes;
+    auto units_of = [&](int b) { return units_in(a, b); };
+    const int chunk = MANY ? (a.B + 31) / 32 : 1, b0 = lane * chunk, b1 = min(a.B, b0 + chunk), n_cta = gridDim.x;
+    const int nu1 = MANY || lane >= a.B ? 0 : units_of(lane);
+    int sum = nu1, some = nu1 > 0;
+    if constexpr (MANY) {
+        for (int b = b0; b < b1; b++) {
+            const int n = units_of(b);
+            sum += n;
+            some += n > 0;
+        }
+    }
+    const int U = __reduce_add_sync(0xffffffffu, sum) * HP;
+    const float N = (float)__reduce_add_sync(0xffffffffu, some) * (float)HP;
+    // (T and the CTAs of a segment need not be exact, only the same in every CTA)
+    const int T = max(kMinUnits, (int)((float)U / (float)n_cta) + 1), more = min((T + 15) >> 4, 8);
+    auto split_ctas = [](int nu, float inv) { return nu == 0 ? 0 : max(1, min(nu, (int)(nu * inv + 0.99f))); };
+    float per_T = 0.0f;                           // 1 / T of a split, else 0
+    if (N <= (float)n_cta) {
+        float inv[4];
+        int k[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            inv[i] = __fdividef(1.0f, (float)(T + i * more));
+            k[i] = split_ctas(nu1, inv[i]);
+        }
+        if constexpr (MANY) {
+            for (int b = b0; b < b1; b++) {
+                const int nu = units_of(b);
+                for (int i = 0; i < 4; i++)
+                    k[i] += split_ctas(nu, inv[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 3; i >= 0; i--)
+            if (__reduce_add_sync(0xffffffffu, k[i]) * HP <= n_cta) {
+                per_T = inv[i];
+                sum = k[i];                       // CTAs instead of units, from here on
+            }
+    }
+    const bool split = per_T > 0.0f;
+    const int per1 = sum;                         // items (CTAs of a split, else units) of the lane's sequence or chunk
+    int before = sum;                             // of those before the lane's
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off)
+            before += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, before, 31) * HP;
+    before -= sum;
+    Plan pl;
+    pl.n_act = split ? all : min(n_cta, (U + kMinUnits - 1) / kMinUnits);
+    pl.split = split;
+    // Item x (each lane its own): its sequence, head-pass, and number within
+    // them; `per` items a segment.
+    auto locate = [&](int x, int &per) {
+        int ci = 0;                               // the lane holding it: the last that begins at or before it
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const int v = __shfl_sync(0xffffffffu, before, ci + off);
+            if ((ci + off) * chunk < a.B && v * HP <= x)
+                ci += off;
+        }
+        int left = x - __shfl_sync(0xffffffffu, before, ci) * HP;
+        Cursor c = {ci * chunk, 0, 0, 0};
+        if constexpr (MANY) {
+            for (; c.b < a.B; c.b++) {
+                c.nu = units_of(c.b);
+                per = split ? split_ctas(c.nu, per_T) : c.nu;
+                if (left < per * HP)
+                    break;
+                left -= per * HP;
+            }
+            per = max(per, 1);
+        } else {
+            c.nu = __shfl_sync(0xffffffffu, nu1, ci);
+            per = max(__shfl_sync(0xffffffffu, per1, ci), 1);
+        }
+        if (HP > 1)
+            c.hp = (unsigned)left / (unsigned)per;
+        c.t = left - c.hp * per;
+        return c;
+    };
+    if (cta < pl.n_act) {
+        Cursor c;
+        int k;
+        if (split) {                              // units counted from the segment's start
+            c = locate(cta, k);
+            const int part = c.t;
+            const Shares sp = {(int)((unsigned)c.nu / (unsigned)k), (int)((unsigned)c.nu % (unsigned)k)};
+            pl.r0 = sp.start(part), pl.r1 = sp.start(part + 1);
+            pl.cf = cta - part, pl.cl = pl.cf + k - 1;
+        } else {
+            pl.line = {(int)((unsigned)U / (unsigned)pl.n_act), (int)((unsigned)U % (unsigned)pl.n_act)};
+            // (lane 0: the share's start, lane 1: its end)
+            int x = pl.line.start(min(cta + lane, pl.n_act));
+            c = locate(min(x, U - 1), k);
+            if (x < U && c.nu <= kSnap)
+                x += 2 * c.t < c.nu ? -c.t : c.nu - c.t;
+            pl.r0 = __shfl_sync(0xffffffffu, x, 0), pl.r1 = __shfl_sync(0xffffffffu, x, 1);
+            pl.cf = pl.cl = 0;
+        }
+        // (warps without units, if any, are the CTA's last: the merge counts on it)
+        const unsigned len = pl.r1 - pl.r0;
+        pl.warps = {(int)(len / W), (int)(len % W)};
+        const int w0 = pl.r0 + pl.warps.start(min(lane, W));
+        if (split)
+            c.t = w0;
+        else
+            c = locate(min(w0, U - 1), k);
+        if (lane < W)
+            place[lane] = c;
+    }
+    if (lane == 0)
+        *plan = pl;
+}
+
 template <int D, int NT, typename O>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const __grid_constant__ Args a)
 {
@@ -286,128 +423,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     pdl_launch_dependents();
     pdl_wait();
 
-    auto length = [&](int b) { return min(max(a.lens[b], 0), a.Tmax); };
-    auto units_of = [&](int b) { return (length(b) + kUnit - 1) / kUnit; };
+    auto length = [&](int b) { return length_of(a, b); };
+    auto units_of = [&](int b) { return units_in(a, b); };
 
     if (warp == 0) {
-        // ------------------------------ how the CTAs share the units ----
-        // lane i sums over its chunk of sequences (of one head and pass)
-        const int chunk = (a.B + 31) / 32, b0 = lane * chunk, b1 = min(a.B, b0 + chunk), n_cta = gridDim.x;
-        int sum = 0, some = 0;
-#pragma unroll 1
-        for (int b = b0; b < b1; b++) {
-            const int n = units_of(b);
-            sum += n;
-            some += n > 0;
-        }
-        const int U = __reduce_add_sync(0xffffffffu, sum) * HP;
-        const long long N = (long long)__reduce_add_sync(0xffffffffu, some) * HP;
-        // Split: every segment has CTAs of its own, ceil(units / T) of them, if
-        // that takes no more than the grid with T at most 24 units (3/16) above
-        // an even share.  Otherwise the line is cut evenly (below), and a CTA that
-        // shares two segments merges twice, 3 us more, the time of 24 units:
-        // 16.5 against 13.5 us at 8 segments of 256 units; but 68 us cut evenly
-        // against 73 at 64 segments of 1024 units, where T would be 69 more.
-        // (Divisions are a tenth of a microsecond each here; T and the CTAs of a
-        // segment need not be exact, only the same in every CTA.)
-        const int T = max(kMinUnits, (int)((float)U / (float)n_cta) + 1);
-        float per_T = 0.0f;                           // 1 / T of a split, else 0
-        auto split_ctas = [](int nu, float inv) { return nu == 0 ? 0 : max(1, min(nu, (int)(nu * inv + 0.99f))); };
-        if (N <= n_cta) {
-            const int more = min((T + 15) >> 4, 8);
-            float inv[4];
-            int k[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                inv[i] = __frcp_rn((float)(T + i * more));
-            for (int b = b0; b < b1; b++) {
-                const int nu = units_of(b);
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    k[i] += split_ctas(nu, inv[i]);
-            }
-#pragma unroll
-            for (int i = 3; i >= 0; i--)
-                if (__reduce_add_sync(0xffffffffu, k[i]) * HP <= n_cta) {
-                    per_T = inv[i];
-                    some = k[i];
-                }
-        }
-        const bool split = per_T > 0.0f;
-        if (split)
-            sum = some;                               // CTAs instead of units, from here on
-        int before = sum;                             // of the chunks before the lane's
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, before, off);
-            if (lane >= off)
-                before += v;
-        }
-        const int all = __shfl_sync(0xffffffffu, before, 31) * HP;
-        before -= sum;
-        Plan pl;
-        pl.n_act = split ? all : min(n_cta, (U + kMinUnits - 1) / kMinUnits);
-        pl.split = split;
-        // Item x (a CTA of a split, else a unit; each lane its own): its sequence,
-        // head-pass, and number within them.
-        auto items_of = [&](int nu) { return split ? split_ctas(nu, per_T) : nu; };
-        auto locate = [&](int x) {
-            int ci = 0;                               // the chunk holding it: the last that begins at or before it
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                const int v = __shfl_sync(0xffffffffu, before, ci + off);
-                if ((ci + off) * chunk < a.B && v * HP <= x)
-                    ci += off;
-            }
-            int left = x - __shfl_sync(0xffffffffu, before, ci) * HP;
-            Cursor c = {ci * chunk, 0, 0, 0};
-            int per = 0;
-            for (; c.b < a.B; c.b++) {
-                c.nu = units_of(c.b);
-                per = items_of(c.nu);
-                if (left < per * HP)
-                    break;
-                left -= per * HP;
-            }
-            if (HP > 1) {
-                per = max(per, 1);
-                c.hp = left / per;
-            }
-            c.t = left - c.hp * per;
-            return c;
-        };
-        if (cta < pl.n_act) {
-            Cursor c;
-            if (split) {                              // units counted from the segment's start
-                c = locate(cta);
-                const int k = items_of(c.nu), part = c.t;
-                const Shares sp = {c.nu / k, c.nu % k};
-                pl.r0 = sp.start(part), pl.r1 = sp.start(part + 1);
-                pl.cf = cta - part, pl.cl = pl.cf + k - 1;
-            } else {
-                pl.line = {U / pl.n_act, U % pl.n_act};
-                // A cut inside a short segment moves to its nearer end: 16 units
-                // more at most, against a merge across CTAs.  (Lane 0: the
-                // share's start, lane 1: its end.)
-                int x = pl.line.start(min(cta + lane, pl.n_act));
-                c = locate(min(x, U - 1));
-                if (x < U && c.nu <= kSnap)
-                    x += 2 * c.t < c.nu ? -c.t : c.nu - c.t;
-                pl.r0 = __shfl_sync(0xffffffffu, x, 0), pl.r1 = __shfl_sync(0xffffffffu, x, 1);
-                pl.cf = pl.cl = 0;
-            }
-            // (warps without units, if any, are the CTA's last: the merge counts on it)
-            pl.warps = {(pl.r1 - pl.r0) / W, (pl.r1 - pl.r0) % W};
-            const int w0 = pl.r0 + pl.warps.start(min(lane, W));
-            if (split)
-                c.t = w0;
-            else
-                c = locate(min(w0, U - 1));
-            if (lane < W)
-                place[lane] = c;
-        }
-        if (lane == 0)
-            plan = pl;
+        if (a.B <= 32)
+            make_plan<false, W>(a, &plan, place);
+        else
+            make_plan<true, W>(a, &plan, place);
     } else {
         // ------------------------------- sequences without positions ----
         for (int b = cta; b < a.B; b += gridDim.x)
