@@ -136,9 +136,10 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *           zero-filled before first use, left zero-filled by every call that
  *           completes; not shared with calls that may run at the same time
  * Rounding: scores, softmax sums and outputs accumulate in fp32 and the codes
- * enter the tensor cores exactly.  With BQ_F16 output each softmax weight times
- * its value scale enters rounded once to fp16 (2^-11 of it at most, as the
- * output itself); with BQ_F32 output it enters as two fp16 terms (2^-21).
+ * enter the tensor cores exactly.  Each softmax weight times its value scale
+ * enters as two fp16 terms (off by 2^-21 of it); with BQ_F16 output and more than
+ * 2^17 cached positions (B * Hkv * Tmax, times the passes that many query rows
+ * take), rounded once to fp16 (2^-11 of it at most, as the output itself).
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE (D, Tmax, Hkv, G, Tq, scale, o_dtype, cache
  * size), BQ_ERR_BATCH (B < 1), BQ_ERR_ALIGN, BQ_ERR_WORKSPACE, BQ_ERR_CUDA. */
 BQ_API int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q, const int32_t *lens,

@@ -394,15 +394,16 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
         *plan = pl;
 }
 
-template <int D, int NT, typename O>
+// TWO: p dV enters as two fp16 terms.
+template <int D, int NT, typename O, bool TWO>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const __grid_constant__ Args a)
 {
     using C = Cfg<D, NT>;
     constexpr int NB = C::kNB, W = C::kWarps, S = C::kSlots;
-    constexpr bool kTwo = sizeof(O) == 4;             // p dV as two fp16 terms
-    // Key codes as u - 8 too: the conversion serves both row tiles, and its zero
-    // points would take 32 registers.
-    constexpr bool kSignedK = NT == 2;
+    // Key codes as u - 8 too: with two row tiles the conversion serves both, and
+    // zero points would take 32 registers; and with two terms the zero point's
+    // cancellation would be the largest error left.
+    constexpr bool kSignedK = NT == 2 || TWO;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Entry entry[2 * W];                    // warp w: 2w (began before its share), 2w + 1
     __shared__ int arrived[2];
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                                 const float p0 = s[r][2 * k + i][0] * dv[i][j], p1 = s[r][2 * k + i][1] * dv[i][j];
                                 const uint32_t w = pack_f16x2(p0, p1);
                                 bh[r][i] = transposed(w);
-                                if constexpr (kTwo)
+                                if constexpr (TWO)
                                     bl[r][i] = transposed(pack_f16x2(p0 - f16_lo(w), p1 - f16_hi(w)));
                             }
                         const uint32_t x0 = x[2 * jj], x1 = x[2 * jj + 1], y0 = x0 >> 8, y1 = x1 >> 8;
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                         for (int r = 0; r < NT; r++) {
                             mma(acc[r][2 * j], e0, e1, e2, e3, bh[r][0], bh[r][1]);
                             mma(acc[r][2 * j + 1], f0, f1, f2, f3, bh[r][0], bh[r][1]);
-                            if constexpr (kTwo) {
+                            if constexpr (TWO) {
                                 mma(acc[r][2 * j], e0, e1, e2, e3, bl[r][0], bl[r][1]);
                                 mma(acc[r][2 * j + 1], f0, f1, f2, f3, bl[r][0], bl[r][1]);
                             }
@@ -951,11 +952,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     }
 }
 
-template <int D, int NT, typename O>
+template <int D, int NT, typename O, bool TWO>
 int32_t launch(Args &a, int grid, void *stream)
 {
     using C = Cfg<D, NT>;
-    const void *kernel = (const void *)attn_q4_kernel<D, NT, O>;
+    const void *kernel = (const void *)attn_q4_kernel<D, NT, O, TWO>;
     static std::atomic<bool> done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
@@ -971,6 +972,14 @@ int32_t launch(Args &a, int grid, void *stream)
                       args) == cudaSuccess
                ? BQ_OK
                : BQ_ERR_CUDA;
+}
+
+template <int D, int NT>
+int32_t launch(Args &a, int grid, bool f16, bool two, void *stream)
+{
+    if (!f16)
+        return launch<D, NT, float, true>(a, grid, stream);
+    return two ? launch<D, NT, __half, true>(a, grid, stream) : launch<D, NT, __half, false>(a, grid, stream);
 }
 
 // 8-row tiles a warp takes of R query rows, in ceil(R / 8 tiles) passes over a
@@ -1050,13 +1059,12 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     a.counters = static_cast<int *>(ws);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + aq::kMaxGrid * sizeof(int));
     const int grid = sms < aq::kMaxGrid ? sms : aq::kMaxGrid;
-    const bool f16 = o_dtype == BQ_F16;
-    if (kv->D == 128) {
-        if (tiles == 1)
-            return f16 ? aq::launch<128, 1, __half>(a, grid, stream) : aq::launch<128, 1, float>(a, grid, stream);
-        return f16 ? aq::launch<128, 2, __half>(a, grid, stream) : aq::launch<128, 2, float>(a, grid, stream);
-    }
-    if (tiles == 1)
-        return f16 ? aq::launch<64, 1, __half>(a, grid, stream) : aq::launch<64, 1, float>(a, grid, stream);
-    return f16 ? aq::launch<64, 2, __half>(a, grid, stream) : aq::launch<64, 2, float>(a, grid, stream);
+    // fp16 output: one rounding of each weight, by at most half a step as the
+    // output's own, adds 0.4 of the output's error; up to 2^17 cached positions
+    // two terms cost 2 to 6% and spare it (8 x 4096: 9.7 and 9.9 us; 2^17: 14.0 and
+    // 14.7), beyond, 9 to 19% (8 x 32768: 18.1 and 19.7; 64 x 32768: 65.5 and 78.3).
+    const bool f16 = o_dtype == BQ_F16, two = rows * passes <= 1 << 17;
+    if (kv->D == 128)
+        return tiles == 1 ? aq::launch<128, 1>(a, grid, f16, two, stream) : aq::launch<128, 2>(a, grid, f16, two, stream);
+    return tiles == 1 ? aq::launch<64, 1>(a, grid, f16, two, stream) : aq::launch<64, 2>(a, grid, f16, two, stream);
 }
