@@ -46,7 +46,8 @@ enum { BQ_F32 = 0, BQ_F16 = 1, BQ_BF16 = 2 };
  *   k_scales, v_scales  fp16 bits [B][Hkv][Tmax][D/32]
  * Device pointers, 16-byte aligned, caller-owned.  D is 64 or 128, Tmax a
  * multiple of 32, B * Hkv * Tmax < 2^31.  144 bytes a position and KV head at
- * D = 128, against 272 for the Q8 cache and 512 in fp16. */
+ * D = 128, against 272 for the Q8 cache and 512 in fp16.  The planes need no
+ * initialisation: no call reads a position past the valid ones into a result. */
 typedef struct bq_kv_cache_q4 {
     uint8_t *k_codes;
     uint16_t *k_scales;
@@ -67,7 +68,7 @@ typedef struct bq_kv_rows {
     int64_t k_batch, k_token, k_head;    /* strides in elements */
     int64_t v_batch, v_token, v_head;
     int32_t dtype;                       /* BQ_F32, BQ_F16 or BQ_BF16: both k and v */
-    int32_t T;                           /* tokens a sequence, 1 .. Tmax */
+    int32_t T;                           /* tokens a sequence, 1 .. min(Tmax, 2^30) */
 } bq_kv_rows;
 
 /* Quantise new keys and values as they are written to the cache: row i of
@@ -78,7 +79,7 @@ typedef struct bq_kv_rows {
  *           bq_attn_decode_q8 (D = 128, Tmax a multiple of 128; the const of
  *           its fields is the reader's view)
  *   rows    source rows (read only)
- *   B, Hkv  sequences and KV heads of the cache and of the rows
+ *   B, Hkv  sequences and KV heads of the cache and of the rows; Hkv <= 65535
  *   start   device int32 [B]: first position written
  *   count   device int32 [B], or NULL: every sequence writes T rows
  * Device status: BQ_ERR_POSITION for rows whose position is outside [0, Tmax)
@@ -129,12 +130,14 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *           result, whatever the cache holds there.
  *   Tq      query tokens a sequence, 1..32
  *   G       query heads per KV head, 1..16
- *   scale   softmax scale, finite
+ *   scale   softmax scale, |scale| <= 1e18 (any sign)
  *   o       device [B][Tq][Hkv*G][D], overwritten; o_dtype BQ_F32 or BQ_F16
- *           (the input type of the next bq_gemv)
+ *           (the input type of the next bq_gemv); must not overlap q
  *   ws      device workspace >= bq_attn_q4_workspace_bytes(D, Tq, G),
  *           zero-filled before first use, left zero-filled by every call that
  *           completes; not shared with calls that may run at the same time
+ *   dev_status  as the other calls'; there is nothing this one reports, and it
+ *           may be NULL
  * Rounding: scores, softmax sums and outputs accumulate in fp32 and the codes
  * enter the tensor cores exactly.  Each softmax weight times its value scale
  * enters as two fp16 terms (off by 2^-21 of it); with BQ_F16 output and more than

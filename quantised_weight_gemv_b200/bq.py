@@ -368,6 +368,8 @@ def kv_cache_q4(k_codes, k_scales, v_codes, v_scales) -> bq_kv_cache_q4:
     if k_codes.dim() != 4:
         raise ValueError("kv_cache_q4: codes must be [B, Hkv, Tmax, D/2]")
     B, Hkv, Tmax, half = k_codes.shape
+    if any(str(t.device) != str(k_codes.device) for t in (k_scales, v_codes, v_scales)):
+        raise ValueError("kv_cache_q4: the planes must be on one device")
     if (tuple(v_codes.shape) != (B, Hkv, Tmax, half) or half not in (32, 64)
             or any(tuple(t.shape) != (B, Hkv, Tmax, half // 16) for t in (k_scales, v_scales))
             or any(not t.is_contiguous() for t in (k_codes, k_scales, v_codes, v_scales))
@@ -426,6 +428,8 @@ def _refuse_rows(fn: str, kv, k, v, start, count, status, write: bool) -> None:
     given = [t for t in (k, v) if t is not None]
     if len(given) < (1 if write else 2):
         raise ValueError(f"{fn}: " + ("k or v must be given" if write else "k and v must be given"))
+    if start is None:
+        raise ValueError(f"{fn}: start must be given")
     _on_device(fn, k=k, v=v, start=start, count=count, status=status)
     T = given[0].shape[1] if given[0].dim() == 4 else -1
     for name, t in (("k", k), ("v", v)):
@@ -472,6 +476,7 @@ def _kv_rows_call(fn: str, kv, k, v, start, count, status, stream, write: bool) 
         good = False
     if not good:
         _refuse_rows(fn, kv, k, v, start, count, status, write)
+        raise ValueError(f"{fn}: arguments do not fit the cache")
     rows = _rows_struct(k, v, dtype, T)
     name = ("bq_kv_read_q" if write else "bq_kv_append_q") + ("4" if isinstance(kv, bq_kv_cache_q4) else "8")
     rc = getattr(_lib or lib(), name)(ctypes.byref(kv), ctypes.byref(rows), B, H, start.data_ptr(),
@@ -500,6 +505,9 @@ def kv_read(kv, k, v, start, count=None, status=None, stream=None) -> None:
 def _refuse_attn(kv, q, lens, G, o, ws, status) -> None:
     if not isinstance(kv, bq_kv_cache_q4) or not hasattr(kv, "B"):
         raise ValueError("attn_decode_q4: kv must come from kv_cache_q4")
+    for name, t in (("q", q), ("lens", lens), ("o", o), ("ws", ws)):
+        if t is None:
+            raise ValueError(f"attn_decode_q4: {name} must be given")
     _on_device("attn_decode_q4", q=q, lens=lens, o=o, ws=ws, status=status)
     B, Hkv = kv.B, kv.Hkv
     want = (B, q.shape[1], Hkv * G, kv.D) if q.dim() == 4 else (B, Hkv * G, kv.D)
@@ -538,6 +546,7 @@ def attn_decode_q4(kv: bq_kv_cache_q4, q, lens, G: int, scale: float, o, ws, sta
         good = False
     if not good:
         _refuse_attn(kv, q, lens, G, o, ws, status)
+        raise ValueError("attn_decode_q4: arguments do not fit the cache")
     rc = (_lib or lib()).bq_attn_decode_q4(
         ctypes.byref(kv), q.data_ptr(), lens.data_ptr(), B, Tq, Hkv, G, scale, o.data_ptr(), od, ws.data_ptr(),
         ws.numel() * ws.element_size(), None if status is None else status.data_ptr(),

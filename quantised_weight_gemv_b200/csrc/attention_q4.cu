@@ -5,16 +5,25 @@
 // Bound: a position of one KV head is 144 bytes (D = 128), read once for its
 // R = Tq * G query rows: 4 D R / 144 flops a byte, so HBM up to about 16 rows;
 // what stands against it is the number of instructions that unpack 256 codes.
+// Measured (D = 128, 8 KV heads, 5 query heads each): 8 sequences of 32768
+// positions 65.5 us, 4.64 TB/s, of which 10 us are the two ends (plan, first
+// loads, merges) and the stream runs at 5.4 TB/s; one of 32768 18 us; one of
+// 4096 9.8 us, nearly all ends.  40 rows (8 query tokens) at 8 x 2.7k positions
+// on average: 39 us, bound by instructions.
 //
 // Work: a unit is 32 positions of one (sequence, KV head).  The valid units of
-// all sequences form one line (lens are on the device, so every warp builds the
-// prefix sums itself); CTAs take equal consecutive shares of it, and a CTA's
-// warps equal consecutive shares of the CTA's.  Ragged lengths
+// all sequences form one line (lens are on the device: one warp of every CTA
+// makes the plan, the others meanwhile clear the outputs of empty sequences).  A
+// segment, one (sequence, KV head), gets CTAs of its own where that fits the
+// grid; else CTAs take equal consecutive shares of the line (see make_plan).  A
+// CTA's warps take equal consecutive shares of the CTA's.  Ragged lengths
 // therefore cost no balance, and a sequence that ends inside a share just
 // starts the next one: a warp never waits for another before its line ends.
 // A warp streams its units through a ring of its own in shared memory with
 // 16-byte cp.async, laid down in a swizzle that keeps ldmatrix free of bank
-// conflicts; no barrier, and nothing that could wait for ever.
+// conflicts; no barrier, and nothing that could wait for ever.  (Copies by TMA,
+// a box of 32 rows of 64 bytes at a time, made 8 x 32768 81 us where these made
+// it 69.)
 //
 // Softmax: one pass with a running reference m a row; a warp's result of a
 // segment (the part of a sequence's head in its share) is (m, l, O).  A whole
@@ -29,11 +38,13 @@
 //     enters times 1/16 there), B = q.  Positions fill the 16-row side, so no
 //     operand is padded.  Each block's sum, less its zero point
 //     8 2^-24 sum(q), is scaled by dK in fp32.  q is multiplied by a power of two
-//     a row first so that both forms are exact.
+//     a row first so that both forms are exact.  Where kSignedK says so: u - 8,
+//     as the values.
 //   values  O^T[d][row]: A = value codes u - 8 (exact fp16: (0x6400 | u) - 1032),
 //     signed so that sums over thousands of positions do not cancel against a
-//     zero-point sum, B = p dV rounded to fp16.  ldmatrix.trans on 16-bit units
-//     turns position-major rows into pairs of positions per register.
+//     zero-point sum, B = p dV as two fp16 terms, or one (TWO: see the end).
+//     ldmatrix.trans on 16-bit units turns position-major rows into pairs of
+//     positions per register.
 //   p dV reaches B's layout by one movmatrix a tile and never leaves registers.
 // Scaling of p: fp16 must neither overflow nor go subnormal where it counts, so
 // a row's reference bounds p dV instead of p: m = max s + log2 dV - 11, with
@@ -153,8 +164,8 @@ __device__ __forceinline__ void row_scales(float (&d)[NB], uint32_t addr)
     else
         asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(d[0]), "=f"(d[1]) : "r"(addr) : "memory");
 }
-// One position's fp16 scales to fp32, shared to shared memory (mask: 0 or ~0);
-// returns the bits of the largest.
+// One position's fp16 scales to fp32, shared to shared memory (live: else zeros);
+// returns the bits of the largest magnitude.
 template <int NB>
 __device__ __forceinline__ uint32_t convert_scales(uint32_t dst, uint32_t src, bool live)
 {
@@ -167,13 +178,13 @@ __device__ __forceinline__ uint32_t convert_scales(uint32_t dst, uint32_t src, b
 #pragma unroll
     for (int i = 0; i < NB / 2; i++) {
         w[i] = live ? w[i] : 0u;
-        mx = __vmaxu2(mx, w[i]);
+        mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
     }
     if constexpr (NB == 4)
         asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "f"(f16_lo(w[0])), "f"(f16_hi(w[0])), "f"(f16_lo(w[1])), "f"(f16_hi(w[1])) : "memory");
     else
         asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(dst), "f"(f16_lo(w[0])), "f"(f16_hi(w[0])) : "memory");
-    return max(mx & 0x7fffu, (mx >> 16) & 0x7fffu);
+    return max(mx & 0xffffu, mx >> 16);
 }
 // 16 bytes to shared memory, past L1.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
@@ -271,8 +282,9 @@ __device__ __forceinline__ int units_in(const Args &a, int b) { return (length_o
 //
 // Up to 32 sequences a lane has one and the plan is straight-line code on
 // registers; beyond, a lane has a chunk of them, and loops over it (MANY).
-// What this costs is fetching instructions that run once: 4.7 us with loops
-// and integer divisions throughout, 1.5 us so.
+// What this costs is fetching instructions that run once: one sequence of 32768
+// positions took 20 us with integer divisions and loops throughout, 19 without
+// the divisions, 18 without the loops.
 template <bool MANY, int W>
 __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *place)
 {
@@ -895,9 +907,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         // share are where the even shares put them: owner() holds there.)
         float *base = a.partials + (size_t)cf * 2 * gp;
         // All partials of a few rows are copied to shared memory at once (the
-        // rings and the warps' partials are done with) and summed there; warps without a sum, or all after
-        // it, clear what was copied.  Loops, not unrolled: this runs once, and
-        // fetching its code is what it would cost.
+        // rings and the warps' partials are done with) and summed there; warps
+        // without a sum, or all after it, clear what was copied.  Loops, not
+        // unrolled: this runs once, and fetching its code is what it would cost.
         const int P = cl - cf + 1;
         const int step = min(32, (C::kRoom / P) & ~1);   // (even, at least 2)
         float *so = reinterpret_cast<float *>(sbase);

@@ -63,7 +63,7 @@ def attention_ref(planes, q_bits, lens, G, scale):
             continue
         for h in range(H // G):
             K, V = deq_q4(kc[b, h, :n], ks[b, h, :n]), deq_q4(vc[b, h, :n], vs[b, h, :n])
-            dk = oracle.half_to_double(ks[b, h, :n])
+            dk = np.abs(oracle.half_to_double(ks[b, h, :n]))
             for i in range(Tq):
                 m = n - (Tq - 1 - i)
                 if m <= 0:
@@ -73,7 +73,7 @@ def attention_ref(planes, q_bits, lens, G, scale):
                     p = np.exp(s - s.max())
                     p /= p.sum()
                     o[b, i, j], ao[b, i, j] = p @ V[:m], p @ np.abs(V[:m])
-                    floor[b, i, j] = m * 2.0 ** -32 * max(oracle.half_to_double(vs[b, h, :m]).max(), 2.0 ** -14)
+                    floor[b, i, j] = m * 2.0 ** -32 * max(np.abs(oracle.half_to_double(vs[b, h, :m])).max(), 2.0 ** -14)
                     S = abs(scale) * 23 * (dk[:m] @ np.abs(q[b, i, j]).reshape(-1, 32).sum(-1)).max()
                     slack[b, i, j] = 2 * 4 * 2.0 ** -23 * S + 2.0 ** -22 * 1.4427 * np.abs(s).max()
     return o, ao, slack, floor

@@ -131,6 +131,49 @@ def test_zero_caches_and_zero_queries():
     assert not o[1].any()
 
 
+@pytest.mark.parametrize("f16", [True, False])
+def test_negative_scales(f16):
+    """Scales of either sign (a cache written by hand): the largest magnitude of
+    a unit's value scales is a negative one's, or a positive one's beside them."""
+    planes = [p.copy() for p in random_cache_q4(21, 2, 2, 128, 128)]
+    planes[1][:, :, ::3] ^= 0x8000
+    planes[3][0, :, ::2] ^= 0x8000
+    planes[3][1, :, 1:] |= 0x8000
+    vs = planes[3].view(np.float16)
+    vs[0, :, 5] *= np.float16(-900)
+    vs[1, :, 0] *= np.float16(900)
+    q = q_bits(22, 2, 1, 8, 128)
+    o = run_attention(planes, q, [128, 100], 4, 0.088, f16)
+    check_attention(o, attention_ref(planes, q, [128, 100], 4, 0.088), f16)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+def test_values_that_are_not_finite_stay_in_their_head_and_query_row(f16):
+    B, Hkv, G, Tmax = 2, 3, 4, 2048
+    planes = random_cache_q4(23, B, Hkv, Tmax, 128)
+    q = q_bits(24, B, 1, Hkv * G, 128)
+    lens = [2000, 70]
+    clean = run_attention(planes, q, lens, G, 0.088, f16)
+    bad = [p.copy() for p in planes]
+    bad[1][0, 1, 777, 2] = 0x7e00                                     # a NaN key scale: head 1 of sequence 0
+    bad[3][1, 2, 33] = 0x7e00                                         # NaN value scales: head 2 of sequence 1
+    o = run_attention(bad, q, lens, G, 0.088, f16).reshape(B, Hkv, G, 128)
+    want = clean.reshape(B, Hkv, G, 128)
+    for b, h in np.ndindex(B, Hkv):
+        if (b, h) in ((0, 1), (1, 2)):
+            assert np.isnan(o[b, h]).all()
+        else:
+            assert np.array_equal(o[b, h], want[b, h])
+    qn = q.copy()
+    qn[0, 0, 5, 9], qn[1, 0, 2, 100] = 0x7e00, 0x7c00                 # NaN, inf
+    o, want = run_attention(planes, qn, lens, G, 0.088, f16), clean
+    for b, i in np.ndindex(B, Hkv * G):
+        if (b, i) in ((0, 5), (1, 2)):
+            assert np.isnan(o[b, 0, i]).all()
+        else:
+            assert np.allclose(o[b, 0, i], want[b, 0, i], rtol=2.0 ** -10, atol=2.0 ** -12)
+
+
 def test_determinism_and_one_workspace_for_all_shapes():
     import torch
     ws = bq.workspace(bq.lib().bq_attn_q4_workspace_bytes(128, 32, 16), DEV)

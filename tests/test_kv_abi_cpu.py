@@ -134,6 +134,10 @@ def test_binding_refuses_wrong_caches():
                 cache_q4(D=96)):
         with pytest.raises(ValueError, match="do not match the cache layout"):
             bq.kv_cache_q4(*bad)
+    other = dev(2, 4, 64, 64, dtype=torch.uint8)
+    other.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="on one device"):
+        bq.kv_cache_q4(kc, ks, other, vs)
 
 
 @pytest.mark.parametrize("call", [bq.kv_append, bq.kv_read])
@@ -155,6 +159,8 @@ def test_binding_refuses_wrong_rows(call):
         call(kv, dev(2, 3, 4, 128, dtype=torch.float64), dev(2, 3, 4, 128, dtype=torch.float64), start)
     with pytest.raises(ValueError, match="start must be int32"):
         call(kv, ok, ok, dev(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="start must be given"):
+        call(kv, ok, ok, None)
     with pytest.raises(ValueError, match="count must be int32"):
         call(kv, ok, ok, start, dev(3, dtype=torch.int32))
     with pytest.raises(ValueError, match="kv must come from"):
@@ -185,6 +191,9 @@ def test_binding_refuses_wrong_attention_arguments():
             f(kv, q, lens, 5, 0.1, bad, ws)
     with pytest.raises(ValueError, match="kv must come from kv_cache_q4"):
         f(object(), q, lens, 5, 0.1, o, ws)
+    for bad in ((None, lens, o, ws), (q, None, o, ws), (q, lens, None, ws), (q, lens, o, None)):
+        with pytest.raises(ValueError, match="must be given"):
+            f(kv, bad[0], bad[1], 5, 0.1, bad[2], bad[3])
 
 
 def test_overlap_rule():
