@@ -144,7 +144,8 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  * 2^17 cached positions (B * Hkv * Tmax, times the passes that many query rows
  * take), rounded once to fp16 (2^-11 of it at most, as the output itself).
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE (D, Tmax, Hkv, G, Tq, scale, o_dtype, cache
- * size), BQ_ERR_BATCH (B < 1), BQ_ERR_ALIGN, BQ_ERR_WORKSPACE, BQ_ERR_CUDA. */
+ * size; also B * Hkv * Tmax * passes >= 2^35, which Tq * G <= 256 never
+ * reaches), BQ_ERR_BATCH (B < 1), BQ_ERR_ALIGN, BQ_ERR_WORKSPACE, BQ_ERR_CUDA. */
 BQ_API int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q, const int32_t *lens,
                                  int32_t B, int32_t Tq, int32_t Hkv, int32_t G, float scale,
                                  void *o, int32_t o_dtype, void *ws, size_t ws_bytes,

@@ -67,7 +67,8 @@ namespace aq {
 constexpr int kUnit = 32;                 // positions per unit
 constexpr int kMaxGrid = 160;             // CTAs (one per SM)
 constexpr int kMinUnits = 8;              // units per CTA, where there are few
-constexpr int kSnap = 32;                 // segments up to this length are never cut between CTAs (see below)
+constexpr int kSnap = 48;                 // segments up to this length are never cut between CTAs (see below)
+constexpr int kEdge = 1;                  // units that a segment's start counts for when the line is cut
 constexpr float kFloor = -3.0e38f;        // a reference no score has reached
 constexpr float kBase = 11.0f, kSlack = 4.0f;
 
@@ -264,6 +265,7 @@ struct Cursor {
 struct Plan {
     int n_act;                            // CTAs with work
     int split;                            // 1: the CTA's segment has CTAs of its own, cf .. cl
+    int edge;                             // units a segment's start counts for on the line (see make_plan)
     int r0, r1, cf, cl;                   // its units (split: counted from the segment's start)
     Shares line, warps;                   // even shares of the line and of r0 .. r1
 };
@@ -277,8 +279,12 @@ __device__ __forceinline__ int units_in(const Args &a, int b) { return (length_o
 // share.  Otherwise the line is cut evenly, and a CTA that shares two segments
 // merges twice, 3 us more, the time of 24 units: 16.5 against 13.5 us at 8
 // segments of 256 units; but 68 us cut evenly against 73 at 64 segments of
-// 1024 units, where T would be 69 more.  A cut inside a short segment moves to
-// its nearer end: 16 units more at most, against a merge across CTAs.
+// 1024 units, where T would be 69 more.  On the line a segment's start (queries
+// read and scaled, outputs written) counts as kEdge units, laid before its
+// first: without that a warp whose share was 14 segments of two units held up
+// the others (256 sequences of 1 to 2048 positions, 8 KV heads: 87 us, so 73;
+// 64 of 1 to 4096: 54 and 43).  A cut inside a short segment moves to its nearer
+// end: 24 units more at most, against a merge across CTAs.
 //
 // Up to 32 sequences a lane has one and the plan is straight-line code on
 // registers; beyond, a lane has a chunk of them, and loops over it (MANY).
@@ -329,6 +335,8 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
             }
     }
     const bool split = per_T > 0.0f;
+    if (!split)
+        sum += some * kEdge;
     const int per1 = sum;                         // items (CTAs of a split, else units) of the lane's sequence or chunk
     int before = sum;                             // of those before the lane's
 #pragma unroll
@@ -340,8 +348,9 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
     const int all = __shfl_sync(0xffffffffu, before, 31) * HP;
     before -= sum;
     Plan pl;
-    pl.n_act = split ? all : min(n_cta, (U + kMinUnits - 1) / kMinUnits);
+    pl.n_act = split ? all : min(n_cta, (all + kMinUnits - 1) / kMinUnits);
     pl.split = split;
+    pl.edge = split ? 0 : kEdge;
     // Item x (each lane its own): its sequence, head-pass, and number within
     // them; `per` items a segment.
     auto locate = [&](int x, int &per) {
@@ -357,7 +366,7 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
         if constexpr (MANY) {
             for (; c.b < a.B; c.b++) {
                 c.nu = units_of(c.b);
-                per = split ? split_ctas(c.nu, per_T) : c.nu;
+                per = split ? split_ctas(c.nu, per_T) : c.nu + (c.nu > 0 ? kEdge : 0);
                 if (left < per * HP)
                     break;
                 left -= per * HP;
@@ -382,12 +391,12 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
             pl.r0 = sp.start(part), pl.r1 = sp.start(part + 1);
             pl.cf = cta - part, pl.cl = pl.cf + k - 1;
         } else {
-            pl.line = {(int)((unsigned)U / (unsigned)pl.n_act), (int)((unsigned)U % (unsigned)pl.n_act)};
+            pl.line = {(int)((unsigned)all / (unsigned)pl.n_act), (int)((unsigned)all % (unsigned)pl.n_act)};
             // (lane 0: the share's start, lane 1: its end)
             int x = pl.line.start(min(cta + lane, pl.n_act));
-            c = locate(min(x, U - 1), k);
-            if (x < U && c.nu <= kSnap)
-                x += 2 * c.t < c.nu ? -c.t : c.nu - c.t;
+            c = locate(min(x, all - 1), k);
+            if (x < all && c.nu <= kSnap)
+                x += 2 * c.t < k ? -c.t : k - c.t;
             pl.r0 = __shfl_sync(0xffffffffu, x, 0), pl.r1 = __shfl_sync(0xffffffffu, x, 1);
             pl.cf = pl.cl = 0;
         }
@@ -398,7 +407,7 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
         if (split)
             c.t = w0;
         else
-            c = locate(min(w0, U - 1), k);
+            c = locate(min(w0, all - 1), k);
         if (lane < W)
             place[lane] = c;
     }
@@ -464,8 +473,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             c.nu = c.b < a.B ? units_of(c.b) : 1;
         } while (c.nu == 0);
     };
-    const int w0 = plan.r0 + plan.warps.start(warp), w1 = plan.r0 + plan.warps.start(warp + 1);
+    const int edge = plan.edge, w1 = plan.r0 + plan.warps.start(warp + 1);
     Cursor cur = place[warp];
+    cur.t -= edge;                                    // (below 0: the segment's start)
+    const int w0 = plan.r0 + plan.warps.start(warp) - min(cur.t, 0);
+    cur.t = max(cur.t, 0);
 
     // ------------------------------------------------------- the ring ----
     // lane i copies chunk i % NB of positions i / NB, + 32 / NB, ... of keys and
@@ -498,6 +510,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 Cursor c = copy_at[warp];
                 if (++c.hp == HP)
                     next_seq(c);
+                to_issue -= edge;
                 is_left = c.nu;
                 is_row = seg_row(c);
                 __syncwarp();
@@ -799,8 +812,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         }
         // the next segment
         cur.t = 0;
-        if (!after && ++cur.hp == HP)
-            next_seq(cur);
+        if (!after) {
+            u += edge;
+            if (++cur.hp == HP)
+                next_seq(cur);
+        }
     }
     __syncthreads();
 
@@ -1039,7 +1055,7 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     const int R = Tq * G;
     const int tiles = aq::tiles_of(R), passes = (R + 8 * tiles - 1) / (8 * tiles);
     // positions, and units of all passes, are 32-bit numbers
-    if (rows >= (1LL << 31) || rows / 32 * passes >= (1LL << 31))
+    if (rows >= (1LL << 31) || rows / 32 * passes >= (1LL << 31) / (1 + aq::kEdge))
         return BQ_ERR_SHAPE;
     if (!aligned16(kv->k_codes) || !aligned16(kv->k_scales) || !aligned16(kv->v_codes) ||
         !aligned16(kv->v_scales) || !aligned16(q) || !aligned16(o) || !aligned16(ws) ||
