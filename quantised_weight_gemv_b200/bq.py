@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -346,17 +347,19 @@ def _one_device(fn: str, **tensors) -> None:
             raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{cur}")
 
 
-_T = None          # torch, its dtypes' codes and current stream's address, once a call has needed them
+_T = None          # what a call needs of torch, looked up once
 
 
 def _torch():
     global _T
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # (current_stream() takes 3 us)
+    # (torch.cuda.current_stream() takes 3 us, current_device() twice what it calls)
+    raw, cur = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     if raw is None:
         def raw(dev):
             return torch.cuda.current_stream(dev).cuda_stream
-    _T = (torch, {torch.float32: BQ_F32, torch.float16: BQ_F16, torch.bfloat16: BQ_BF16}, raw)
+    _T = (torch.int32, {torch.float32: BQ_F32, torch.float16: BQ_F16, torch.bfloat16: BQ_BF16}, raw,
+          cur or torch.cuda.current_device, (torch.float16, torch.int16, torch.uint16))
     return _T
 
 
@@ -401,22 +404,17 @@ def _overlaps(shape, strides) -> bool:
     return False
 
 
-def _rows_struct(k, v, dtype: int, T: int) -> bq_kv_rows:
-    # (a stride over an extent of 1 is never used)
-    if T > 1:
-        kb, kt, kh = (0, 0, 0) if k is None else k.stride()[:3]
-        vb, vt, vh = (0, 0, 0) if v is None else v.stride()[:3]
-    else:
-        kt = vt = 0
-        kb, _, kh = (0, 0, 0) if k is None else k.stride()[:3]
-        vb, _, vh = (0, 0, 0) if v is None else v.stride()[:3]
-    t = k if k is not None else v
-    if t.shape[0] == 1:
-        kb = vb = 0
-    if t.shape[2] == 1:
-        kh = vh = 0
-    return bq_kv_rows(0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
-                      kb, kt, kh, vb, vt, vh, dtype, T)
+_ROWS = struct.Struct("=QQqqqqqqii")              # a bq_kv_rows
+_NO_ROWS = (0, 0, 0, 1)
+_rows_fns = {}                                    # (cache type, read?) -> function whose structs are plain addresses
+
+
+def _rows_fn(kind, write: bool):
+    name = ("bq_kv_read_q" if write else "bq_kv_append_q") + ("4" if kind is bq_kv_cache_q4 else "8")
+    f = lib()[name]                               # (a function object of its own)
+    f.restype, f.argtypes = _i32, [_vp, _vp, *_KV_SIGS[name][1][2:]]
+    _rows_fns[kind, write] = f
+    return f
 
 
 def _refuse_rows(fn: str, kv, k, v, start, count, status, write: bool) -> None:
@@ -454,37 +452,44 @@ def _refuse_rows(fn: str, kv, k, v, start, count, status, write: bool) -> None:
 def _kv_rows_call(fn: str, kv, k, v, start, count, status, stream, write: bool) -> None:
     # One pass over what has to hold (this runs once a layer and token); what
     # does not is named by _refuse_rows.
-    torch, codes, raw_stream = _T or _torch()
+    int32, codes, raw_stream, current, _ = _T or _torch()
     try:
         t = v if k is None else k
-        B, T, H, D = t.shape
+        shape = t.shape
+        B, T, H, D = shape
         dtype = codes[t.dtype]
         dev = kv._refs[0].get_device()
-        good = (dev >= 0 and B == kv.B and H == kv.Hkv and D == kv.D and T > 0 and t.stride(3) == 1
-                and (v is None or v is t or (v.shape == t.shape and v.dtype is t.dtype and v.stride(3) == 1))
+        kp, (kb, kt, kh, k1) = (0, _NO_ROWS) if k is None else (k.data_ptr(), k.stride())
+        vp, (vb, vt, vh, v1) = (0, _NO_ROWS) if v is None else (v.data_ptr(), v.stride())
+        good = (type(kv) in (bq_kv_cache, bq_kv_cache_q4) and dev >= 0 and k1 == 1 and v1 == 1 and B == kv.B and H == kv.Hkv and D == kv.D and 0 < T < 1 << 31
+                and (v is t or v is None or (v.shape == shape and v.dtype is t.dtype and v.get_device() == dev))
                 and (write or (k is not None and v is not None))
-                and (not write or ((k is None or k.is_contiguous() or not _overlaps(k.shape, k.stride()))
-                                   and (v is None or v.is_contiguous() or not _overlaps(v.shape, v.stride()))))
-                and start.dtype is torch.int32 and start.numel() == B and start.is_contiguous()
-                and (count is None or (count.dtype is torch.int32 and count.numel() == B and count.is_contiguous()
+                and (not write or ((k is None or k.is_contiguous() or not _overlaps(shape, k.stride()))
+                                   and (v is None or v.is_contiguous() or not _overlaps(shape, v.stride()))))
+                and start.dtype is int32 and start.numel() == B and start.is_contiguous()
+                and (count is None or (count.dtype is int32 and count.numel() == B and count.is_contiguous()
                                        and count.get_device() == dev))
                 and (status is None or (status.get_device() == dev and status.element_size() == 4
                                         and status.numel() > 0))
-                and t.get_device() == dev and (v is None or v.get_device() == dev) and start.get_device() == dev
-                and torch.cuda.current_device() == dev)
+                and t.get_device() == dev and start.get_device() == dev and current() == dev)
     except (AttributeError, KeyError, TypeError, ValueError):
         good = False
     if not good:
         _refuse_rows(fn, kv, k, v, start, count, status, write)
         raise ValueError(f"{fn}: arguments do not fit the cache")
-    rows = _rows_struct(k, v, dtype, T)
-    name = ("bq_kv_read_q" if write else "bq_kv_append_q") + ("4" if isinstance(kv, bq_kv_cache_q4) else "8")
-    rc = getattr(_lib or lib(), name)(ctypes.byref(kv), ctypes.byref(rows), B, H, start.data_ptr(),
-                                      None if count is None else count.data_ptr(),
-                                      None if status is None else status.data_ptr(),
-                                      raw_stream(dev) if stream is None else stream.cuda_stream)
+    # (a stride over an extent of 1 is never used)
+    if T == 1:
+        kt = vt = 0
+    if B == 1:
+        kb = vb = 0
+    if H == 1:
+        kh = vh = 0
+    f = _rows_fns.get((type(kv), write)) or _rows_fn(type(kv), write)
+    rc = f(ctypes.byref(kv), _ROWS.pack(kp, vp, kb, kt, kh, vb, vt, vh, dtype, T), B, H, start.data_ptr(),
+           None if count is None else count.data_ptr(), None if status is None else status.data_ptr(),
+           raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
-        check(name, rc)
+        check(f.__name__, rc)
 
 
 def kv_append(kv, k, v, start, count=None, status=None, stream=None) -> None:
@@ -528,7 +533,7 @@ def attn_decode_q4(kv: bq_kv_cache_q4, q, lens, G: int, scale: float, o, ws, sta
     o are [B, Hkv*G, D] (one query token a sequence) or [B, Tq, Hkv*G, D]; q
     fp16 bits, o fp32 or fp16.  Query token i of sequence b attends to the
     positions below lens[b] - (Tq - 1 - i)."""
-    torch, codes, raw_stream = _T or _torch()
+    _, codes, raw_stream, current, half_bits = _T or _torch()
     try:
         shape, dev = q.shape, kv._refs[0].get_device()
         B, Hkv = kv.B, kv.Hkv
@@ -536,12 +541,11 @@ def attn_decode_q4(kv: bq_kv_cache_q4, q, lens, G: int, scale: float, o, ws, sta
         od = codes[o.dtype]
         good = (dev >= 0 and type(kv) is bq_kv_cache_q4 and len(shape) in (3, 4) and shape[0] == B and shape[-2] == Hkv * G
                 and shape[-1] == kv.D and o.shape == shape and od != BQ_BF16
-                and (q.dtype is torch.float16 or q.dtype is torch.int16 or q.dtype is torch.uint16)
-                and lens.dtype is torch.int32 and lens.numel() == B
+                and q.dtype in half_bits and lens.dtype is _T[0] and lens.numel() == B
                 and q.is_contiguous() and o.is_contiguous() and lens.is_contiguous() and ws.is_contiguous()
                 and q.get_device() == dev and o.get_device() == dev and lens.get_device() == dev
                 and ws.get_device() == dev and (status is None or status.get_device() == dev)
-                and torch.cuda.current_device() == dev)
+                and current() == dev)
     except (AttributeError, KeyError, TypeError, ValueError):
         good = False
     if not good:
