@@ -6,10 +6,10 @@
 // R = Tq * G query rows: 4 D R / 144 flops a byte, so HBM up to about 16 rows;
 // what stands against it is the number of instructions that unpack 256 codes.
 // Measured (D = 128, 8 KV heads, 5 query heads each): 8 sequences of 32768
-// positions 65.5 us, 4.64 TB/s, of which 10 us are the two ends (plan, first
-// loads, merges) and the stream runs at 5.4 TB/s; one of 32768 18 us; one of
-// 4096 9.8 us, nearly all ends.  40 rows (8 query tokens) at 8 x 2.7k positions
-// on average: 39 us, bound by instructions.
+// positions 61 us, 4.96 TB/s, of which 10 us are the two ends (plan, first
+// loads, merges) and the stream runs at 5.9 TB/s; one of 32768 18 us; one of
+// 4096 10 us, nearly all ends.  40 rows (8 query tokens) at 8 x 2.7k positions
+// on average: 37 us, bound by instructions.
 //
 // Work: a unit is 32 positions of one (sequence, KV head).  The valid units of
 // all sequences form one line (lens are on the device: one warp of every CTA
@@ -117,6 +117,23 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Two fp32 operations in one instruction: x = x a + c, a b, x + y.
+__device__ __forceinline__ void fma2(float (&x)[2], float a0, float a1, float c0, float c1)
+{
+    asm("{.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %5};\n\t"
+        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;}"
+        : "+f"(x[0]), "+f"(x[1]) : "f"(a0), "f"(a1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float (&x)[2], float a0, float a1, float b)
+{
+    asm("{.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;}"
+        : "=f"(x[0]), "=f"(x[1]) : "f"(a0), "f"(a1), "f"(b));
+}
+__device__ __forceinline__ void add2(float (&x)[2], const float (&y)[2])
+{
+    asm("{.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;}"
+        : "+f"(x[0]), "+f"(x[1]) : "f"(y[0]), "f"(y[1]));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
@@ -658,11 +675,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll
                     for (int r = 0; r < NT; r++)
 #pragma unroll
-                        for (int i = 0; i < 2; i++)
-#pragma unroll
-                            for (int e = 0; e < 2; e++)
-                                s[r][2 * mt + i][e] = j == 0 ? dk[i][0] * c[r][2 * i + e]
-                                                             : fmaf(dk[i][j], c[r][2 * i + e], s[r][2 * mt + i][e]);
+                        for (int i = 0; i < 2; i++) {
+                            float (&sp)[2] = s[r][2 * mt + i];
+                            if (j == 0) {
+                                mul2(sp, c[r][2 * i], c[r][2 * i + 1], dk[i][0]);
+                            } else {
+                                float cp[2] = {c[r][2 * i], c[r][2 * i + 1]};
+                                fma2(cp, dk[i][j], dk[i][j], sp[0], sp[1]);
+                                sp[0] = cp[0], sp[1] = cp[1];
+                            }
+                        }
                 }
             }
             if (t0 + kUnit > L - (a.Tq - 1)) {    // some row's positions end in this unit
@@ -677,16 +699,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             // --------------------------------- running reference ----
             // the unit's bound on log2(dV), and per row on s + log2(dV) - kBase
             const float eb = fmaf((float)vmax, 0x1p-10f, -15.0f - kBase);
+            // (of the lane's positions: the whole row's is needed only where m moves)
             bool grow = false;
             float cand[NT][2];
 #pragma unroll
             for (int r = 0; r < NT; r++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    float mx = fmaxf(fmaxf(s[r][0][e], s[r][1][e]), fmaxf(s[r][2][e], s[r][3][e]));
-#pragma unroll
-                    for (int off = 4; off < 32; off <<= 1)
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const float mx = fmaxf(fmaxf(s[r][0][e], s[r][1][e]), fmaxf(s[r][2][e], s[r][3][e]));
                     cand[r][e] = __fmaf_ru(mx, mul[r][e], eb);   // (rounded up: scores of any size keep p dV in range)
                     grow = grow || cand[r][e] - m[r][e] > kSlack;
                 }
@@ -695,6 +715,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 for (int r = 0; r < NT; r++)
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1)
+                            cand[r][e] = fmaxf(cand[r][e], __shfl_xor_sync(0xffffffffu, cand[r][e], off));
                         const float mn = fmaxf(m[r][e], cand[r][e]), f = ex2(m[r][e] - mn);
                         m[r][e] = mn;
                         l[r][e] *= f;
@@ -708,13 +731,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll
             for (int r = 0; r < NT; r++)
 #pragma unroll
-                for (int p = 0; p < 4; p++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        float &w = s[r][p][e];
-                        w = ex2(fmaf(w, mul[r][e], -m[r][e]));
-                        l[r][e] += w;
-                    }
+                for (int p = 0; p < 4; p++) {
+                    fma2(s[r][p], mul[r][0], mul[r][1], -m[r][0], -m[r][1]);
+                    s[r][p][0] = ex2(s[r][p][0]);
+                    s[r][p][1] = ex2(s[r][p][1]);
+                    add2(l[r], s[r][p]);
+                }
             // ------------------------------------------ values ----
 #pragma unroll
             for (int k = 0; k < 2; k++) {         // 16 positions
@@ -733,11 +755,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                         for (int r = 0; r < NT; r++)
 #pragma unroll
                             for (int i = 0; i < 2; i++) {
-                                const float p0 = s[r][2 * k + i][0] * dv[i][j], p1 = s[r][2 * k + i][1] * dv[i][j];
-                                const uint32_t w = pack_f16x2(p0, p1);
+                                float pv[2];
+                                mul2(pv, s[r][2 * k + i][0], s[r][2 * k + i][1], dv[i][j]);
+                                const uint32_t w = pack_f16x2(pv[0], pv[1]);
                                 bh[r][i] = transposed(w);
                                 if constexpr (TWO)
-                                    bl[r][i] = transposed(pack_f16x2(p0 - f16_lo(w), p1 - f16_hi(w)));
+                                    bl[r][i] = transposed(pack_f16x2(pv[0] - f16_lo(w), pv[1] - f16_hi(w)));
                             }
                         const uint32_t x0 = x[2 * jj], x1 = x[2 * jj + 1], y0 = x0 >> 8, y1 = x1 >> 8;
                         const uint32_t e0 = nib_lo(x0), e1 = nib_hi(x0), e2 = nib_lo(x1), e3 = nib_hi(x1);
