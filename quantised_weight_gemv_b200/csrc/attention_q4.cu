@@ -8,7 +8,7 @@
 // Measured (D = 128, 8 KV heads, 5 query heads each): 8 sequences of 32768
 // positions 61 us, 4.96 TB/s, of which 10 us are the two ends (plan, first
 // loads, merges) and the stream runs at 5.9 TB/s; one of 32768 18 us; one of
-// 4096 10 us, nearly all ends.  40 rows (8 query tokens) at 8 x 2.7k positions
+// 4096 10 us, nearly all ends.  40 rows (8 query tokens) at 8 x 3k positions
 // on average: 37 us, bound by instructions.
 //
 // Work: a unit is 32 positions of one (sequence, KV head).  The valid units of
@@ -1034,18 +1034,18 @@ int32_t launch(Args &a, int grid, bool f16, bool two, void *stream)
 }
 
 // 8-row tiles a warp takes of R query rows, in ceil(R / 8 tiles) passes over a
-// segment.  At 64 segments of 8192 positions (D = 128) a further pass takes 12.4
+// segment.  At 64 segments of 8192 positions (D = 128) a further pass takes 11.8
 // us with one tile; with two, which unpack codes once for both but run 2 warps a
-// scheduler instead of 4, 21.5.  So 24 rows take 55 us in three passes and 61 in
-// two, 40 rows 79 and 82, but 16 rows 42 and 37, 48 rows 92 and 84, and from 7
+// scheduler instead of 4, 19.9.  So 24 rows take 52 us in three passes and 56 in
+// two, 40 rows 75 and 76, but 16 rows 39 and 35, 48 rows 87 and 77, and from 6
 // tiles on two a pass are no slower.  (Tiles side by side in a CTA, over one copy
-// of the cache in L2 or shared memory, were no faster: 60 and 64 us at 24 and 32
-// rows, 93 at 40; at 302 MB of cache, past L2, 180, 190 and 286 against 165, 185
-// and 263.)
+// of the cache in L2 or shared memory, were no faster when these took 55, 63 and
+// 79 us at 24, 32 and 40 rows: 60, 64 and 93; at 302 MB of cache, past L2, 180,
+// 190 and 286 against 165, 185 and 263.)
 int tiles_of(int R)
 {
     const int t = (R + 7) / 8;
-    return 173 * ((t + 1) / 2) < 100 * t ? 2 : 1;
+    return 169 * ((t + 1) / 2) < 100 * t ? 2 : 1;
 }
 
 }  // namespace aq
@@ -1112,8 +1112,8 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     const int grid = sms < aq::kMaxGrid ? sms : aq::kMaxGrid;
     // fp16 output: one rounding of each weight, by at most half a step as the
     // output's own, adds 0.4 of the output's error; up to 2^17 cached positions
-    // two terms cost 2 to 6% and spare it (8 x 4096: 9.7 and 9.9 us; 2^17: 14.0 and
-    // 14.7), beyond, 9 to 19% (8 x 32768: 18.1 and 19.7; 64 x 32768: 65.5 and 78.3).
+    // two terms cost 2 to 6% and spare it (8 x 4096: 9.8 and 10.0 us; 2^17: 14.0 and
+    // 14.8), beyond, 10 to 22% (8 x 32768: 17.9 and 19.7; 64 x 32768: 63 and 77).
     const bool f16 = o_dtype == BQ_F16, two = rows * passes <= 1 << 17;
     if (kv->D == 128)
         return tiles == 1 ? aq::launch<128, 1>(a, grid, f16, two, stream) : aq::launch<128, 2>(a, grid, f16, two, stream);
