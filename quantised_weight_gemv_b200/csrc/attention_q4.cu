@@ -290,6 +290,20 @@ struct Plan {
 __device__ __forceinline__ int length_of(const Args &a, int b) { return min(max(a.lens[b], 0), a.Tmax); }
 __device__ __forceinline__ int units_in(const Args &a, int b) { return (length_of(a, b) + kUnit - 1) / kUnit; }
 
+// f(units) for each of a lane's sequences b0 .. b1 - 1: in registers (PER), or read.
+template <int PER, typename F>
+__device__ __forceinline__ void each_own(const Args &a, const int (&own)[PER ? PER : 1], int b0, int b1, F f)
+{
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+            f(own[i]);
+    } else {
+        for (int b = b0; b < b1; b++)
+            f(units_in(a, b));
+    }
+}
+
 // ---------------------------------- how the CTAs share the units ----
 // Split: every segment has CTAs of its own, about units / T of them, if that
 // takes no more than the grid with T at most 24 units (3/16) above an even
@@ -303,26 +317,28 @@ __device__ __forceinline__ int units_in(const Args &a, int b) { return (length_o
 // 64 of 1 to 4096: 54 and 43).  A cut inside a short segment moves to its nearer
 // end: 24 units more at most, against a merge across CTAs.
 //
-// Up to 32 sequences a lane has one and the plan is straight-line code on
-// registers; beyond, a lane has a chunk of them, and loops over it (MANY).
-// What this costs is fetching instructions that run once: one sequence of 32768
-// positions took 20 us with integer divisions and loops throughout, 19 without
-// the divisions, 18 without the loops.
-template <bool MANY, int W>
+// Up to 32 sequences a lane has one, up to 128 PER = 4, and the plan is
+// straight-line code on registers; beyond (PER = 0), a lane has a chunk of them,
+// and loops over it.  What this costs is fetching instructions that run once: one
+// sequence of 32768 positions took 20 us with integer divisions and loops
+// throughout, 19 without the divisions, 18 without the loops; 128 sequences of 512
+// 17.0 us with loops, 16.5 without.  (Their units laid out in shared memory first:
+// 1024 sequences of one unit 12.9 instead of 14.5 us, but all small calls 0.1 to
+// 0.2 us more for the code in between.)
+template <int PER, int W>
 __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *place)
 {
-    const int lane = threadIdx.x & 31, cta = blockIdx.x, HP = a.Hkv * a.passes;
-    auto units_of = [&](int b) { return units_in(a, b); };
-    const int chunk = MANY ? (a.B + 31) / 32 : 1, b0 = lane * chunk, b1 = min(a.B, b0 + chunk), n_cta = gridDim.x;
-    const int nu1 = MANY || lane >= a.B ? 0 : units_of(lane);
-    int sum = nu1, some = nu1 > 0;
-    if constexpr (MANY) {
-        for (int b = b0; b < b1; b++) {
-            const int n = units_of(b);
-            sum += n;
-            some += n > 0;
-        }
-    }
+    const int lane = threadIdx.x & 31, cta = blockIdx.x, HP = a.Hkv * a.passes, n_cta = gridDim.x;
+    const int chunk = PER ? PER : (a.B + 31) / 32, b0 = lane * chunk, b1 = min(a.B, b0 + chunk);
+    int own[PER ? PER : 1];                       // the lane's sequences' units
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        own[i] = b0 + i < a.B ? units_in(a, b0 + i) : 0;
+    int sum = 0, some = 0;                        // (sum: units, later items, of one of the HP segments)
+    each_own<PER>(a, own, b0, b1, [&](int n) {
+        sum += n;
+        some += n > 0;
+    });
     const int U = __reduce_add_sync(0xffffffffu, sum) * HP;
     const float N = (float)__reduce_add_sync(0xffffffffu, some) * (float)HP;
     // (T and the CTAs of a segment need not be exact, only the same in every CTA)
@@ -333,17 +349,13 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
         float inv[4];
         int k[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < 4; i++)
             inv[i] = __fdividef(1.0f, (float)(T + i * more));
-            k[i] = split_ctas(nu1, inv[i]);
-        }
-        if constexpr (MANY) {
-            for (int b = b0; b < b1; b++) {
-                const int nu = units_of(b);
-                for (int i = 0; i < 4; i++)
-                    k[i] += split_ctas(nu, inv[i]);
-            }
-        }
+        each_own<PER>(a, own, b0, b1, [&](int n) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                k[i] += split_ctas(n, inv[i]);
+        });
 #pragma unroll
         for (int i = 3; i >= 0; i--)
             if (__reduce_add_sync(0xffffffffu, k[i]) * HP <= n_cta) {
@@ -352,10 +364,10 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
             }
     }
     const bool split = per_T > 0.0f;
+    auto items = [&](int nu) { return split ? split_ctas(nu, per_T) : nu + (nu > 0 ? kEdge : 0); };   // of a segment
     if (!split)
         sum += some * kEdge;
-    const int per1 = sum;                         // items (CTAs of a split, else units) of the lane's sequence or chunk
-    int before = sum;                             // of those before the lane's
+    int before = sum;                             // items of the sequences before the lane's
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, before, off);
@@ -380,19 +392,29 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
         }
         int left = x - __shfl_sync(0xffffffffu, before, ci) * HP;
         Cursor c = {ci * chunk, 0, 0, 0};
-        if constexpr (MANY) {
+        if constexpr (PER > 0) {
+            c.nu = __shfl_sync(0xffffffffu, own[0], ci);
+            per = items(c.nu);
+#pragma unroll
+            for (int i = 1; i < PER; i++) {
+                const int n = __shfl_sync(0xffffffffu, own[i], ci);
+                if (c.b == ci * PER + i - 1 && left >= per * HP) {
+                    left -= per * HP;
+                    c.b++;
+                    c.nu = n;
+                    per = items(n);
+                }
+            }
+        } else {
             for (; c.b < a.B; c.b++) {
-                c.nu = units_of(c.b);
-                per = split ? split_ctas(c.nu, per_T) : c.nu + (c.nu > 0 ? kEdge : 0);
+                c.nu = units_in(a, c.b);
+                per = items(c.nu);
                 if (left < per * HP)
                     break;
                 left -= per * HP;
             }
-            per = max(per, 1);
-        } else {
-            c.nu = __shfl_sync(0xffffffffu, nu1, ci);
-            per = max(__shfl_sync(0xffffffffu, per1, ci), 1);
         }
+        per = max(per, 1);
         if (HP > 1)
             c.hp = (unsigned)left / (unsigned)per;
         c.t = left - c.hp * per;
@@ -467,9 +489,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 
     if (warp == 0) {
         if (a.B <= 32)
-            make_plan<false, W>(a, &plan, place);
+            make_plan<1, W>(a, &plan, place);
+        else if (a.B <= 128)
+            make_plan<4, W>(a, &plan, place);
         else
-            make_plan<true, W>(a, &plan, place);
+            make_plan<0, W>(a, &plan, place);
     } else {
         // ------------------------------- sequences without positions ----
         for (int b = cta; b < a.B; b += gridDim.x)

@@ -47,6 +47,13 @@ CASES = [
     (100, 1, 3, 2, 64, 1024, [(37 * i) % 1025 for i in range(100)]),
     (70, 1, 1, 5, 128, 4096, [4096 if i % 9 == 4 else (11 * i) % 200 for i in range(70)]),
     (33, 2, 4, 3, 128, 1056, [1056 - i for i in range(33)]),
+    # numbers of sequences around those a plan's lane holds, empty ones among them
+    (32, 1, 2, 2, 64, 256, [(91 * i) % 257 for i in range(32)]),
+    (64, 1, 2, 4, 64, 512, [(i % 5 != 0) * ((77 * i) % 513) for i in range(64)]),
+    (128, 1, 1, 3, 128, 320, [(i > 60) * ((53 * i) % 321) for i in range(128)]),
+    (128, 1, 1, 1, 64, 2048, [2048 if i in (3, 77, 127) else 0 for i in range(128)]),
+    (129, 1, 2, 1, 64, 96, [(29 * i) % 97 for i in range(129)]),
+    (130, 1, 1, 2, 64, 4096, [4000 if i in (0, 64, 129) else 0 for i in range(130)]),
 ]
 
 
