@@ -10,10 +10,10 @@
 // instructions: at 16-bit rows the SMs have about 14 a lane and element.
 // Measured at 16384 tokens of 8 heads of 128 (copy peak 6.45 TB/s; 2 to 4 us of
 // each are the launch's ends):
-//   from or to fp32:   Q4 append 28.8 us (5.3 TB/s), read 27.1 (5.6);
-//                      Q8 append 36.7 (4.6), read 29.2 (5.8)
-//   fp16 or bf16:      Q4 append 18.9 (4.5), read 17.8 (4.8);
-//                      Q8 append 25.9 (4.0), read 19.7 (5.2)
+//   from or to fp32:   Q4 append 28.2 us (5.4 TB/s), read 27.1 (5.6);
+//                      Q8 append 33.9 (5.0), read 29.2 (5.8)
+//   fp16 or bf16:      Q4 append 18.0 (4.8), read 17.8 (4.8);
+//                      Q8 append 22.1 (4.6), read 19.7 (5.2)
 // and 1.6 to 2.7 us for a token of 8 x 8 rows, the time of a launch.  A
 // thread moves 8 elements of a key row and the same 8 of the value row, four
 // threads a block (its maximum takes two shuffles), so a row's threads read and
@@ -215,12 +215,20 @@ struct Lane {
     __device__ __forceinline__ int element() const { return 32 * blk + 4 * jj; }
 };
 
+// Blocks an SM that the appends' registers leave room for, beside the 16-byte
+// loads in flight a thread: fp32 rows, 2 loads of which are a row's 8 elements, run
+// more threads (16384 tokens, Q4 and Q8: 28.2 and 33.9 us; 4 blocks 28.8 and 34.4;
+// 8 x 1300 tokens 10.3 and 12.4, 4 blocks 12.4 and 14.9), 16-bit rows all loads of
+// four rows (18.0 and 22.1 us; two rows 18.9 and 23.6).
+template <typename E>
+constexpr int kBlocks = sizeof(E) == 4 ? 5 : 4;
+
 // One block: a tile of tokens of one head, for every sequence in turn of
 // gridDim.y.  blockDim / (D / 8) rows at a time, ROWS times: 4 where that leaves
 // every SM two full blocks, else 1 (a decode step's few rows finish sooner side
 // by side).
 template <int D, typename E, int ROWS>
-__global__ void __launch_bounds__(kThreads) append_q4_kernel(const Args a)
+__global__ void __launch_bounds__(kThreads, kBlocks<E>) append_q4_kernel(const Args a)
 {
     pdl_launch_dependents();
     pdl_wait();
@@ -237,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) append_q4_kernel(const Args a)
         const E *vp = static_cast<const E *>(a.r.v) + b * a.r.v_batch + h * a.r.v_head + t.element() + min(i0, a.T - 1) * a.r.v_token;
         const int64_t k_step = at_once * a.r.k_token, v_step = at_once * a.r.v_token;
         bool fine = true;
-        constexpr int U = ROWS == 1 || sizeof(E) == 4 ? 1 : 2;      // rows whose loads are in flight together
+        constexpr int U = ROWS == 1 || sizeof(E) == 4 ? 1 : 4;      // rows whose loads are in flight together
 #pragma unroll 1
         for (int i = i0; i < i0 + ROWS * at_once; i += U * at_once) {
             Raw<E, 16> x[U][2];
@@ -336,7 +344,7 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t *p)
 // where they belong: 2.6 us for a token of 8 x 8 rows, where the tile took 1.7
 // more.
 template <typename E>
-__global__ void __launch_bounds__(kThreads, 3) append_q8_kernel(const Args a)
+__global__ void __launch_bounds__(kThreads, kBlocks<E>) append_q8_kernel(const Args a)
 {
     constexpr int D = 128, kLanes = D / 8, kGap = Place<E>::kGap;
     __shared__ alignas(16) uint32_t vt[D * kTile / 4];
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_q8_kernel(const Args a)
         }
         uint32_t vc[4][2];
         if ((threadIdx.x / 32 + 1) * 8 > t.lo && threadIdx.x / 32 * 8 < t.hi) {   // the warp has a position
-            constexpr int U = sizeof(E) == 4 ? 1 : 2;
+            constexpr int U = sizeof(E) == 4 ? 1 : 4;
 #pragma unroll
             for (int s0 = 0; s0 < 4; s0 += U) {
                 Raw<E, kGap> x[U][2];
