@@ -244,6 +244,56 @@ def test_positions_outside_the_cache_are_skipped_and_reported(fmt, start, count,
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("src", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_every_16_bit_magnitude_as_a_block_maximum(fmt, src):
+    """Block i's largest magnitude is 16-bit pattern i, its other elements random
+    parts of it: scales (subnormal and zero ones among them) and codes are the
+    quantiser's; blocks whose scale overflows fp16 are zeros and reported."""
+    import torch
+    top = np.arange(0x7c00 if src == "f16" else 0x7f80, dtype=np.uint16)
+    top = torch.from_numpy(np.resize(top, -(-top.size // 8) * 8).view(np.int16)).view(dtype(src)).float().numpy()
+    f = np.random.default_rng(16).uniform(-1, 1, (top.size, 32)).astype(np.float32)
+    f[np.arange(top.size), np.arange(top.size) % 32] = 1
+    f[::2] = np.sign(f[::2]) * np.rint(np.abs(f[::2]) * 14) / 14             # (many near halves)
+    x = torch.from_numpy(f * top[:, None]).to(dtype(src)).reshape(1, -1, 2, 128)
+    n = x.shape[1]
+    Tmax = -(-n // 128) * 128
+    kv = make_kv(fmt, new_cache(fmt, 1, 2, Tmax, 128))
+    st = status()
+    bq.kv_append(kv, x.to(DEV), x.to(DEV), ints([0]), None, st)
+    xf = x.float().numpy().copy()
+    blocks = xf.reshape(-1, 32)
+    over = np.abs(blocks).max(1) / np.float32(7 if fmt == 4 else 127) >= 65520
+    blocks[over] = 0
+    assert int(st.item()) == (1 << bq.BQ_ERR_RANGE if over.any() else 0)
+    for got, w in zip(planes_of(kv), place(fmt, new_cache(fmt, 1, 2, Tmax, 128), xf, xf, [0], [n])):
+        assert np.array_equal(got, w)
+
+
+@pytest.mark.parametrize("src", ["f32", "f16"])
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_two_streams_append_neighbouring_positions(fmt, src):
+    """Two calls at once into one cache, whose ranges meet inside a value tile
+    and inside a word of transposed value bytes, many times over."""
+    import torch
+    B, H, Tmax, D = 2, 4, 512, 128
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for cut in (37, 130, 255):
+        kv = make_kv(fmt, new_cache(fmt, B, H, Tmax, D))
+        k, v, kf, vf = rows(cut, B, 400, H, D, src)
+        n = 400 - cut
+        args = [(k[:, :cut], v[:, :cut], ints([3] * B)), (k[:, cut:], v[:, cut:], ints([3 + cut] * B))]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for s, (kk, vv, start) in zip(streams, args):
+                bq.kv_append(kv, kk, vv, start, stream=s)
+        torch.cuda.synchronize()
+        want = place(fmt, new_cache(fmt, B, H, Tmax, D), kf, vf, [3] * B, [cut + n] * B)
+        for got, w in zip(planes_of(kv), want):
+            assert np.array_equal(got, w)
+
+
 def test_broadcast_rows_and_a_single_token_of_a_longer_tensor():
     """Stride 0 over tokens (one row written to every position), and a T = 1
     slice whose unused strides are odd."""
