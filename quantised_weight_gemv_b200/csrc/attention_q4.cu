@@ -66,7 +66,8 @@ namespace aq {
 
 constexpr int kUnit = 32;                 // positions per unit
 constexpr int kMaxGrid = 160;             // CTAs (one per SM)
-constexpr int kMinUnits = 8;              // units per CTA, where there are few
+constexpr int kMinUnits[2] = {4, 8};      // units per CTA of 16 or 8 warps, where there are few,
+constexpr int kWhole = 12;                // and units up to which segments are whole then (see make_plan)
 constexpr int kSnap = 48;                 // segments up to this length are never cut between CTAs (see below)
 constexpr int kEdge = 1;                  // units that a segment's start counts for when the line is cut
 constexpr float kFloor = -3.0e38f;        // a reference no score has reached
@@ -317,6 +318,11 @@ __device__ __forceinline__ void each_own(const Args &a, const int (&own)[PER ? P
 // 64 of 1 to 4096: 54 and 43).  A cut inside a short segment moves to its nearer
 // end: 24 units more at most, against a merge across CTAs.
 //
+// Few units: where no segment has more than 12, each keeps one CTA (8 segments of
+// 12 units 7.5 us; split 8.5); else a CTA of 16 warps takes 4 at least (8 segments
+// of 16 units 8.5 us; with 8 at least 9.0), one of 8 warps 8 (64 query rows over 2
+// segments of 64 units 15.4 us; with 4 at least 16.6).
+//
 // Up to 32 sequences a lane has one, up to 128 PER = 4, and the plan is
 // straight-line code on registers; beyond (PER = 0), a lane has a chunk of them,
 // and loops over it.  What this costs is fetching instructions that run once: one
@@ -334,15 +340,18 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
 #pragma unroll
     for (int i = 0; i < PER; i++)
         own[i] = b0 + i < a.B ? units_in(a, b0 + i) : 0;
-    int sum = 0, some = 0;                        // (sum: units, later items, of one of the HP segments)
+    int sum = 0, some = 0, longest = 0;           // (sum: units, later items, of one of the HP segments)
     each_own<PER>(a, own, b0, b1, [&](int n) {
         sum += n;
         some += n > 0;
+        longest = max(longest, n);
     });
+    constexpr int kMin = kMinUnits[W < 16];
+    const int least = __reduce_max_sync(0xffffffffu, longest) <= kWhole ? kWhole : kMin;
     const int U = __reduce_add_sync(0xffffffffu, sum) * HP;
     const float N = (float)__reduce_add_sync(0xffffffffu, some) * (float)HP;
     // (T and the CTAs of a segment need not be exact, only the same in every CTA)
-    const int T = max(kMinUnits, (int)((float)U / (float)n_cta) + 1), more = min((T + 15) >> 4, 8);
+    const int T = max(least, (int)((float)U / (float)n_cta) + 1), more = min((T + 15) >> 4, 8);
     auto split_ctas = [](int nu, float inv) { return nu == 0 ? 0 : max(1, min(nu, (int)(nu * inv + 0.99f))); };
     float per_T = 0.0f;                           // 1 / T of a split, else 0
     if (N <= (float)n_cta) {
@@ -377,7 +386,7 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
     const int all = __shfl_sync(0xffffffffu, before, 31) * HP;
     before -= sum;
     Plan pl;
-    pl.n_act = split ? all : min(n_cta, (all + kMinUnits - 1) / kMinUnits);
+    pl.n_act = split ? all : min(n_cta, (all + kMin - 1) / kMin);
     pl.split = split;
     pl.edge = split ? 0 : kEdge;
     // Item x (each lane its own): its sequence, head-pass, and number within

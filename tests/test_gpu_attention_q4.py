@@ -47,6 +47,12 @@ CASES = [
     (100, 1, 3, 2, 64, 1024, [(37 * i) % 1025 for i in range(100)]),
     (70, 1, 1, 5, 128, 4096, [4096 if i % 9 == 4 else (11 * i) % 200 for i in range(70)]),
     (33, 2, 4, 3, 128, 1056, [1056 - i for i in range(33)]),
+    # segments kept whole or split where there are few units
+    (1, 1, 2, 4, 128, 384, [384]),
+    (1, 1, 2, 4, 128, 416, [413]),
+    (3, 1, 2, 2, 64, 512, [12, 385, 512]),
+    (2, 4, 1, 12, 128, 1024, [1024, 350]),
+    (1, 8, 2, 8, 128, 640, [640]),
     # numbers of sequences around those a plan's lane holds, empty ones among them
     (32, 1, 2, 2, 64, 256, [(91 * i) % 257 for i in range(32)]),
     (64, 1, 2, 4, 64, 512, [(i % 5 != 0) * ((77 * i) % 513) for i in range(64)]),
