@@ -47,6 +47,9 @@ CASES = [
     (100, 1, 3, 2, 64, 1024, [(37 * i) % 1025 for i in range(100)]),
     (70, 1, 1, 5, 128, 4096, [4096 if i % 9 == 4 else (11 * i) % 200 for i in range(70)]),
     (33, 2, 4, 3, 128, 1056, [1056 - i for i in range(33)]),
+    # two row tiles a warp with one fp16 term a weight (more than 2^17 cached positions)
+    (4, 4, 3, 4, 128, 16384, [16384, 100, 9001, 0]),
+    (5, 3, 2, 8, 64, 16384, [2, 16383, 700, 12000, 33]),
     # segments kept whole or split where there are few units
     (1, 1, 2, 4, 128, 384, [384]),
     (1, 1, 2, 4, 128, 416, [413]),

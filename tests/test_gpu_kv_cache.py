@@ -86,6 +86,9 @@ APPENDS = [
     (4, 2, 37, 2, 128, 64, [11, 27], [37, 5]),
     (4, 2, 64, 3, 64, 64, [0, 0], [64, 0]),
     (4, 1, 1025, 4, 128, 2048, [777], None),
+    # enough rows for four a thread
+    (4, 2, 2051, 5, 128, 2112, [13, 0], [2051, 1999]),
+    (4, 3, 2600, 5, 64, 2624, [24, 0, 7], [2600, 0, 2593]),
     (8, 1, 1, 1, 128, 128, [127], None),
     (8, 4, 1, 3, 128, 256, [0, 63, 64, 200], [1, 1, 0, 1]),
     (8, 2, 37, 2, 128, 128, [11, 91], [37, 5]),
