@@ -140,9 +140,9 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *           may be NULL
  * Rounding: scores, softmax sums and outputs accumulate in fp32 and the codes
  * enter the tensor cores exactly.  Each softmax weight times its value scale
- * enters as two fp16 terms (off by 2^-21 of it); with BQ_F16 output and more than
- * 2^17 cached positions (B * Hkv * Tmax, times the passes that many query rows
- * take), rounded once to fp16 (2^-11 of it at most, as the output itself).
+ * enters as two fp16 terms: off by 2^-21 of it or, where that is more, by 2^-35
+ * of the largest value scale (2^-14 at least) below lens[b].  BQ_F16 output is
+ * the BQ_F32 output rounded once.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE (D, Tmax, Hkv, G, Tq, scale, o_dtype, cache
  * size; also B * Hkv * Tmax * passes >= 2^35, which Tq * G <= 256 never
  * reaches), BQ_ERR_BATCH (B < 1), BQ_ERR_ALIGN, BQ_ERR_WORKSPACE, BQ_ERR_CUDA. */

@@ -5,11 +5,11 @@
 // Bound: a position of one KV head is 144 bytes (D = 128), read once for its
 // R = Tq * G query rows: 4 D R / 144 flops a byte, so HBM up to about 16 rows;
 // what stands against it is the number of instructions that unpack 256 codes.
-// Measured (D = 128, 8 KV heads, 5 query heads each): 8 sequences of 32768
-// positions 61 us, 4.96 TB/s, of which 10 us are the two ends (plan, first
-// loads, merges) and the stream runs at 5.9 TB/s; one of 32768 18 us; one of
-// 4096 10 us, nearly all ends.  40 rows (8 query tokens) at 8 x 3k positions
-// on average: 37 us, bound by instructions.
+// Measured in a chain of graph launches (D = 128, 8 KV heads, 5 query heads
+// each): 8 sequences of 32768 positions 75 us, 4.0 TB/s, of which 10 us are the
+// two ends (plan, first loads, merges); one of 32768 21 us; one of 4096 10 us,
+// nearly all ends.  40 rows (8 query tokens) at 8 x 3k positions on average:
+// 43 us, bound by instructions.
 //
 // Work: a unit is 32 positions of one (sequence, KV head).  The valid units of
 // all sequences form one line (lens are on the device: one warp of every CTA
@@ -33,18 +33,18 @@
 //
 // Tensor cores (mma.sync m16n8k16; with 8 or 16 rows a tcgen05 tile of 128
 // rows would be empty), fp32 accumulation, codes exact:
-//   scores  S^T[t][row]: A = key codes u (0..15) as fp16 subnormals u 2^-24 (the
-//     masked nibble is the whole conversion; the high nibble is 16 u, so q
-//     enters times 1/16 there), B = q.  Positions fill the 16-row side, so no
-//     operand is padded.  Each block's sum, less its zero point
-//     8 2^-24 sum(q), is scaled by dK in fp32.  q is multiplied by a power of two
-//     a row first so that both forms are exact.  Where kSignedK says so: u - 8,
-//     as the values.
-//   values  O^T[d][row]: A = value codes u - 8 (exact fp16: (0x6400 | u) - 1032),
-//     signed so that sums over thousands of positions do not cancel against a
-//     zero-point sum, B = p dV as two fp16 terms, or one (TWO: see the end).
-//     ldmatrix.trans on 16-bit units turns position-major rows into pairs of
-//     positions per register.
+//   scores  S^T[t][row]: A = key codes u - 8 (exact fp16: (0x6400 | u) - 1032),
+//     B = q.  Positions fill the 16-row side, so no operand is padded.  Each
+//     block's sum is scaled by dK in fp32.  q is multiplied by a power of two a
+//     row first, so that subnormal queries are exact too.  (Signed codes: with
+//     unsigned ones the zero point's cancellation would be the largest error.)
+//   values  O^T[d][row]: A = value codes u - 8, signed so that sums over
+//     thousands of positions do not cancel against a zero-point sum, B = p dV as
+//     two fp16 terms, whatever the output's type: one term would round every
+//     weight as coarsely as a 16-bit output is rounded, 1.4 times the error of
+//     the output's own rounding (8 x 32768 positions: 2.9e-4 of the result instead
+//     of 2.1e-4, in 61 us instead of 75).  ldmatrix.trans on 16-bit units turns
+//     position-major rows into pairs of positions per register.
 //   p dV reaches B's layout by one movmatrix a tile and never leaves registers.
 // Scaling of p: fp16 must neither overflow nor go subnormal where it counts, so
 // a row's reference bounds p dV instead of p: m = max s + log2 dV - 11, with
@@ -157,13 +157,6 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-// (started at c, whose registers stay)
-__device__ __forceinline__ void mma_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -238,12 +231,6 @@ __device__ __forceinline__ uint32_t nib_hi(uint32_t x)
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h) : "r"(h), "r"(0x2C002C00u), "r"(0xD480D480u));   // / 16 - 72
     return h;
 }
-
-// Code pairs as fp16: SIGNED: u - 8; else the masked bits, subnormals u 2^-24 (16 u 2^-24).
-template <bool SIGNED>
-__device__ __forceinline__ uint32_t code_lo(uint32_t x) { return SIGNED ? nib_lo(x) : x & 0x000F000Fu; }
-template <bool SIGNED>
-__device__ __forceinline__ uint32_t code_hi(uint32_t x) { return SIGNED ? nib_hi(x) : x & 0x00F000F0u; }
 
 // Units shared by CTAs: q each, one more for the first r.
 struct Shares {
@@ -463,16 +450,11 @@ __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *pla
         *plan = pl;
 }
 
-// TWO: p dV enters as two fp16 terms.
-template <int D, int NT, typename O, bool TWO>
+template <int D, int NT, typename O>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const __grid_constant__ Args a)
 {
     using C = Cfg<D, NT>;
     constexpr int NB = C::kNB, W = C::kWarps, S = C::kSlots;
-    // Key codes as u - 8 too: with two row tiles the conversion serves both, and
-    // zero points would take 32 registers; and with two terms the zero point's
-    // cancellation would be the largest error left.
-    constexpr bool kSignedK = NT == 2 || TWO;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Entry entry[2 * W];                    // warp w: 2w (began before its share), 2w + 1
     __shared__ int arrived[2];
@@ -585,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         // nibbles); the lane's row is g of each tile.  What follows a score is
         // held for the accumulator's rows, 2 t4 + e.
         uint32_t qf[NT][NB][2][2];
-        float mul[NT][2], koff[NT][kSignedK ? 1 : NB][4];
+        float mul[NT][2];
         int lim[NT][2];                               // positions a row sees
         uint2 v[NT][NB][2];
         int tok[NT];
@@ -621,28 +603,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             const int k = top == 0 || top >= 0x7c00 ? 0 : 28 - max(top >> 10, 1);
             const float f = a.scale2 < 0.0f ? -pow2i(k) : pow2i(k);
             // positive, so that a masked score of -inf stays one
-            const float back = fmaxf(fabsf(a.scale2) * pow2i((kSignedK ? 0 : 24) - k), 1e-37f);
+            const float back = fmaxf(fabsf(a.scale2) * pow2i(-k), 1e-37f);
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 mul[r][e] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4 * e);
                 lim[r][e] = L - (a.Tq - 1 - __shfl_sync(0xffffffffu, tok[r], 8 * t4 + 4 * e));
             }
 #pragma unroll
-            for (int j = 0; j < NB; j++) {
-                float (&z)[4] = koff[r][kSignedK ? 0 : j];
-                z[0] = z[1] = z[2] = z[3] = 0.0f;
+            for (int j = 0; j < NB; j++)
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
-                    const float fh = hf && !kSignedK ? f * 0.0625f : f;
                     // register e holds elements 4 t4 + e and 4 t4 + 2 + e: the order of the masked key bytes
-                    qf[r][j][hf][0] = pack_f16x2(f16_lo(v[r][j][hf].x) * fh, f16_lo(v[r][j][hf].y) * fh);
-                    qf[r][j][hf][1] = pack_f16x2(f16_hi(v[r][j][hf].x) * fh, f16_hi(v[r][j][hf].y) * fh);
-                    if constexpr (!kSignedK) {        // -8 2^-24 (-128 2^-24) as fp16 subnormals
-                        const uint32_t zp = hf ? 0x80808080u : 0x80088008u;
-                        mma(z, zp, zp, zp, zp, qf[r][j][hf][0], qf[r][j][hf][1]);
-                    }
+                    qf[r][j][hf][0] = pack_f16x2(f16_lo(v[r][j][hf].x) * f, f16_lo(v[r][j][hf].y) * f);
+                    qf[r][j][hf][1] = pack_f16x2(f16_hi(v[r][j][hf].x) * f, f16_hi(v[r][j][hf].y) * f);
                 }
-            }
         }
         float m[NT][2], l[NT][2], acc[NT][2 * NB][4];
 #pragma unroll
@@ -690,18 +664,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll
                 for (int j = 0; j < NB; j++) {
                     const uint32_t x0 = kx[0][j], x1 = kx[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
-                    const uint32_t l0 = code_lo<kSignedK>(x0), l1 = code_lo<kSignedK>(x1);
-                    const uint32_t l2 = code_lo<kSignedK>(y0), l3 = code_lo<kSignedK>(y1);
-                    const uint32_t h0 = code_hi<kSignedK>(x0), h1 = code_hi<kSignedK>(x1);
-                    const uint32_t h2 = code_hi<kSignedK>(y0), h3 = code_hi<kSignedK>(y1);
+                    const uint32_t l0 = nib_lo(x0), l1 = nib_lo(x1), l2 = nib_lo(y0), l3 = nib_lo(y1);
+                    const uint32_t h0 = nib_hi(x0), h1 = nib_hi(x1), h2 = nib_hi(y0), h3 = nib_hi(y1);
                     float c[NT][4];
 #pragma unroll
-                    for (int r = 0; r < NT; r++) {
-                        if constexpr (kSignedK)
-                            mma0(c[r], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
-                        else
-                            mma_from(c[r], koff[r][j], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
-                    }
+                    for (int r = 0; r < NT; r++)
+                        mma0(c[r], l0, l1, l2, l3, qf[r][j][0][0], qf[r][j][0][1]);
 #pragma unroll
                     for (int r = 0; r < NT; r++)
                         mma(c[r], h0, h1, h2, h3, qf[r][j][1][0], qf[r][j][1][1]);
@@ -792,8 +760,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                                 mul2(pv, s[r][2 * k + i][0], s[r][2 * k + i][1], dv[i][j]);
                                 const uint32_t w = pack_f16x2(pv[0], pv[1]);
                                 bh[r][i] = transposed(w);
-                                if constexpr (TWO)
-                                    bl[r][i] = transposed(pack_f16x2(pv[0] - f16_lo(w), pv[1] - f16_hi(w)));
+                                bl[r][i] = transposed(pack_f16x2(pv[0] - f16_lo(w), pv[1] - f16_hi(w)));
                             }
                         const uint32_t x0 = x[2 * jj], x1 = x[2 * jj + 1], y0 = x0 >> 8, y1 = x1 >> 8;
                         const uint32_t e0 = nib_lo(x0), e1 = nib_hi(x0), e2 = nib_lo(x1), e3 = nib_hi(x1);
@@ -802,10 +769,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                         for (int r = 0; r < NT; r++) {
                             mma(acc[r][2 * j], e0, e1, e2, e3, bh[r][0], bh[r][1]);
                             mma(acc[r][2 * j + 1], f0, f1, f2, f3, bh[r][0], bh[r][1]);
-                            if constexpr (TWO) {
-                                mma(acc[r][2 * j], e0, e1, e2, e3, bl[r][0], bl[r][1]);
-                                mma(acc[r][2 * j + 1], f0, f1, f2, f3, bl[r][0], bl[r][1]);
-                            }
+                            mma(acc[r][2 * j], e0, e1, e2, e3, bl[r][0], bl[r][1]);
+                            mma(acc[r][2 * j + 1], f0, f1, f2, f3, bl[r][0], bl[r][1]);
                         }
                     }
                 }
@@ -1036,11 +1001,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
     }
 }
 
-template <int D, int NT, typename O, bool TWO>
+template <int D, int NT, typename O>
 int32_t launch(Args &a, int grid, void *stream)
 {
     using C = Cfg<D, NT>;
-    const void *kernel = (const void *)attn_q4_kernel<D, NT, O, TWO>;
+    const void *kernel = (const void *)attn_q4_kernel<D, NT, O>;
     static std::atomic<bool> done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
@@ -1059,11 +1024,9 @@ int32_t launch(Args &a, int grid, void *stream)
 }
 
 template <int D, int NT>
-int32_t launch(Args &a, int grid, bool f16, bool two, void *stream)
+int32_t launch(Args &a, int grid, bool f16, void *stream)
 {
-    if (!f16)
-        return launch<D, NT, float, true>(a, grid, stream);
-    return two ? launch<D, NT, __half, true>(a, grid, stream) : launch<D, NT, __half, false>(a, grid, stream);
+    return f16 ? launch<D, NT, __half>(a, grid, stream) : launch<D, NT, float>(a, grid, stream);
 }
 
 // 8-row tiles a warp takes of R query rows, in ceil(R / 8 tiles) passes over a
@@ -1143,12 +1106,8 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     a.counters = static_cast<int *>(ws);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + aq::kMaxGrid * sizeof(int));
     const int grid = sms < aq::kMaxGrid ? sms : aq::kMaxGrid;
-    // fp16 output: one rounding of each weight, by at most half a step as the
-    // output's own, adds 0.4 of the output's error; up to 2^17 cached positions
-    // two terms cost 2 to 6% and spare it (8 x 4096: 9.8 and 10.0 us; 2^17: 14.0 and
-    // 14.8), beyond, 10 to 22% (8 x 32768: 17.9 and 19.7; 64 x 32768: 63 and 77).
-    const bool f16 = o_dtype == BQ_F16, two = rows * passes <= 1 << 17;
+    const bool f16 = o_dtype == BQ_F16;
     if (kv->D == 128)
-        return tiles == 1 ? aq::launch<128, 1>(a, grid, f16, two, stream) : aq::launch<128, 2>(a, grid, f16, two, stream);
-    return tiles == 1 ? aq::launch<64, 1>(a, grid, f16, two, stream) : aq::launch<64, 2>(a, grid, f16, two, stream);
+        return tiles == 1 ? aq::launch<128, 1>(a, grid, f16, stream) : aq::launch<128, 2>(a, grid, f16, stream);
+    return tiles == 1 ? aq::launch<64, 1>(a, grid, f16, stream) : aq::launch<64, 2>(a, grid, f16, stream);
 }
