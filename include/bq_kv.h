@@ -130,7 +130,7 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *           result, whatever the cache holds there.
  *   Tq      query tokens a sequence, 1..32
  *   G       query heads per KV head, 1..16
- *   scale   softmax scale, |scale| <= 1e18 (any sign)
+ *   scale   softmax scale, |scale| <= 1e18 (any sign; below 1e-28 as 1e-28)
  *   o       device [B][Tq][Hkv*G][D], overwritten; o_dtype BQ_F32 or BQ_F16
  *           (the input type of the next bq_gemv); must not overlap q
  *   ws      device workspace >= bq_attn_q4_workspace_bytes(D, Tq, G),
@@ -139,7 +139,8 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *   dev_status  as the other calls'; there is nothing this one reports, and it
  *           may be NULL
  * Rounding: scores, softmax sums and outputs accumulate in fp32 and the codes
- * enter the tensor cores exactly.  Each softmax weight times its value scale
+ * enter the tensor cores exactly.  Weights are made from differences of unscaled
+ * scores, so scores may be of any size.  Each softmax weight times its value scale
  * enters as two fp16 terms: off by 2^-21 of it or, where that is more, by 2^-35
  * of the largest value scale (2^-14 at least) below lens[b].  BQ_F16 output is
  * the BQ_F32 output rounded once.

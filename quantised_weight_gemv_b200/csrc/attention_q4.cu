@@ -25,7 +25,7 @@
 // a box of 32 rows of 64 bytes at a time, made 8 x 32768 81 us where these made
 // it 69.)
 //
-// Softmax: one pass with a running reference m a row; a warp's result of a
+// Softmax: one pass with a running maximum m a row; a warp's result of a
 // segment (the part of a sequence's head in its share) is (m, l, O).  A whole
 // segment is written out directly.  The two that may continue in a neighbour
 // are merged at the end: warps through shared memory, CTAs through the
@@ -46,11 +46,12 @@
 //     of 2.1e-4, in 61 us instead of 75).  ldmatrix.trans on 16-bit units turns
 //     position-major rows into pairs of positions per register.
 //   p dV reaches B's layout by one movmatrix a tile and never leaves registers.
-// Scaling of p: fp16 must neither overflow nor go subnormal where it counts, so
-// a row's reference bounds p dV instead of p: m = max s + log2 dV - 11, with
-// log2 of a unit's largest value scale taken as bits / 1024 - 15 (at most 0.09
-// low, up to 9 high for subnormals).  O and l carry the same 2^-m.  m moves
-// only when the bound outgrows it by 2^4: p dV < 2^15.1.
+// Exponents: p = 2^((s - m) scale log2(e)) with s and m still unscaled sums, so
+// that scores of any size keep their differences (a scaled maximum of 2^28 would
+// be rounded by 32, and weights by 2^32).  m moves only when a score outgrows it
+// by 2^4.  p dV must neither overflow fp16 nor go subnormal where it counts: the
+// value scales are taken times 2^(25 - e), e the largest of their exponent bits so
+// far, so that p dV < 2^15.  Both are exact: O and l scale by powers of two alone.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -70,8 +71,10 @@ constexpr int kMinUnits[2] = {4, 8};      // units per CTA of 16 or 8 warps, whe
 constexpr int kWhole = 12;                // and units up to which segments are whole then (see make_plan)
 constexpr int kSnap = 48;                 // segments up to this length are never cut between CTAs (see below)
 constexpr int kEdge = 1;                  // units that a segment's start counts for when the line is cut
-constexpr float kFloor = -3.0e38f;        // a reference no score has reached
-constexpr float kBase = 11.0f, kSlack = 4.0f;
+constexpr float kFloor = -5.0e37f;        // a maximum no score has reached (times 4 finite; times any scale a long way down)
+constexpr float kSlack = 4.0f;
+constexpr int kBase = 25;                 // scales enter times 2^(25 - exponent bits): below 2^11
+constexpr float kScaleMin = 1.0e-28f;     // softmax scales below leave every score below 2^-49
 
 // D: head width; NT: 8-row tiles per warp (1 or 2: see tiles_of).
 template <int D, int NT>
@@ -104,7 +107,7 @@ struct Args {
     int B, Tq, Hkv, G, Tmax;
     int R;                                // Tq * G query rows per KV head
     int passes;                           // of 8 NT rows each
-    float scale2;                         // scale * log2(e)
+    float scale2;                         // scale * log2(e), kScaleMin at least
     int *counters;                        // [grid], by a shared segment's first CTA
     float *partials;                      // [grid][2]: O [rows][D], then (m, l) [rows]
 };
@@ -119,7 +122,7 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Two fp32 operations in one instruction: x = x a + c, a b, x + y.
+// Two fp32 operations in one instruction: x = x a + c, a b, x a, x + y, x - y.
 __device__ __forceinline__ void fma2(float (&x)[2], float a0, float a1, float c0, float c1)
 {
     asm("{.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %5};\n\t"
@@ -131,11 +134,16 @@ __device__ __forceinline__ void mul2(float (&x)[2], float a0, float a1, float b)
     asm("{.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmul.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;}"
         : "=f"(x[0]), "=f"(x[1]) : "f"(a0), "f"(a1), "f"(b));
 }
-__device__ __forceinline__ void add2(float (&x)[2], const float (&y)[2])
-{
-    asm("{.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;}"
-        : "+f"(x[0]), "+f"(x[1]) : "f"(y[0]), "f"(y[1]));
-}
+#define BQ_F32X2(name, op)                                                                                             \
+    __device__ __forceinline__ void name(float (&x)[2], const float (&y)[2])                                           \
+    {                                                                                                                  \
+        asm("{.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t" op ".rn.f32x2 u, u, v;\n\t"         \
+            "mov.b64 {%0, %1}, u;}" : "+f"(x[0]), "+f"(x[1]) : "f"(y[0]), "f"(y[1]));                                  \
+    }
+BQ_F32X2(mul2, "mul")
+BQ_F32X2(add2, "add")
+BQ_F32X2(sub2, "sub")
+#undef BQ_F32X2
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     uint32_t r;
@@ -176,12 +184,10 @@ __device__ __forceinline__ void row_scales(float (&d)[NB], uint32_t addr)
     else
         asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(d[0]), "=f"(d[1]) : "r"(addr) : "memory");
 }
-// One position's fp16 scales to fp32, shared to shared memory (live: else zeros);
-// returns the bits of the largest magnitude.
+// Scales of a position in fp16, or zeros (not live); the bits of the largest magnitude.
 template <int NB>
-__device__ __forceinline__ uint32_t convert_scales(uint32_t dst, uint32_t src, bool live)
+__device__ __forceinline__ uint32_t load_scales(uint32_t (&w)[NB / 2], uint32_t src, bool live)
 {
-    uint32_t w[NB / 2];
     if constexpr (NB == 4)
         asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
     else
@@ -192,11 +198,16 @@ __device__ __forceinline__ uint32_t convert_scales(uint32_t dst, uint32_t src, b
         w[i] = live ? w[i] : 0u;
         mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
     }
-    if constexpr (NB == 4)
-        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "f"(f16_lo(w[0])), "f"(f16_hi(w[0])), "f"(f16_lo(w[1])), "f"(f16_hi(w[1])) : "memory");
-    else
-        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(dst), "f"(f16_lo(w[0])), "f"(f16_hi(w[0])) : "memory");
     return max(mx & 0xffffu, mx >> 16);
+}
+// The same in fp32 times f.
+template <int NB>
+__device__ __forceinline__ void store_scales(uint32_t dst, const uint32_t (&w)[NB / 2], float f)
+{
+    if constexpr (NB == 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "f"(f16_lo(w[0]) * f), "f"(f16_hi(w[0]) * f), "f"(f16_lo(w[1]) * f), "f"(f16_hi(w[1]) * f) : "memory");
+    else
+        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(dst), "f"(f16_lo(w[0]) * f), "f"(f16_hi(w[0]) * f) : "memory");
 }
 // 16 bytes to shared memory, past L1.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
@@ -602,8 +613,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             // max |q| 2^k in [2^13, 2^14) (exact for subnormal rows too); inf and NaN pass through
             const int k = top == 0 || top >= 0x7c00 ? 0 : 28 - max(top >> 10, 1);
             const float f = a.scale2 < 0.0f ? -pow2i(k) : pow2i(k);
-            // positive, so that a masked score of -inf stays one
-            const float back = fmaxf(fabsf(a.scale2) * pow2i(-k), 1e-37f);
+            // positive and not 0, so that a masked score of -inf stays one
+            const float back = fabsf(a.scale2) * pow2i(-k);
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 mul[r][e] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4 * e);
@@ -619,6 +630,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 }
         }
         float m[NT][2], l[NT][2], acc[NT][2 * NB][4];
+        int ev = 0;                                   // exponent bits of the largest value scale so far
 #pragma unroll
         for (int r = 0; r < NT; r++) {
             m[r][0] = m[r][1] = kFloor;
@@ -637,9 +649,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             // lane i converts position i's; past the length the cache may
             // hold anything: scales of 0
             const bool valid = t0 + lane < L;
-            (void)convert_scales<NB>(conv + lane * NB * 4, kb + 2 * C::kCodes + lane * NB * 2, valid);
-            const uint32_t vmax = __reduce_max_sync(
-                0xffffffffu, convert_scales<NB>(conv + (kUnit + lane) * NB * 4, kb + 2 * C::kCodes + C::kScales + lane * NB * 2, valid));
+            uint32_t sc[NB / 2];
+            (void)load_scales<NB>(sc, kb + 2 * C::kCodes + lane * NB * 2, valid);
+            store_scales<NB>(conv + lane * NB * 4, sc, 1.0f);
+            const int top = (int)__reduce_max_sync(
+                0xffffffffu, load_scales<NB>(sc, kb + 2 * C::kCodes + C::kScales + lane * NB * 2, valid)) >> 10;
+            const int en = max(ev, top);
+            store_scales<NB>(conv + (kUnit + lane) * NB * 4, sc, pow2i(kBase - en));
             __syncwarp();
             // ------------------------------------------ scores ----
             // s[r][p][e]: row 2 t4 + e of tile r, position 8 p + g
@@ -697,35 +713,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                         for (int e = 0; e < 2; e++)
                             s[r][p][e] = t0 + 8 * p + g < lim[r][e] ? s[r][p][e] : -INFINITY;
             }
-            // --------------------------------- running reference ----
-            // the unit's bound on log2(dV), and per row on s + log2(dV) - kBase
-            const float eb = fmaf((float)vmax, 0x1p-10f, -15.0f - kBase);
+            // ----------------------------------- running maximum ----
             // (of the lane's positions: the whole row's is needed only where m moves)
-            bool grow = false;
-            float cand[NT][2];
+            bool grow = en > ev;
+            float mx[NT][2];
 #pragma unroll
             for (int r = 0; r < NT; r++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const float mx = fmaxf(fmaxf(s[r][0][e], s[r][1][e]), fmaxf(s[r][2][e], s[r][3][e]));
-                    cand[r][e] = __fmaf_ru(mx, mul[r][e], eb);   // (rounded up: scores of any size keep p dV in range)
-                    grow = grow || cand[r][e] - m[r][e] > kSlack;
+                    mx[r][e] = fmaxf(fmaxf(s[r][0][e], s[r][1][e]), fmaxf(s[r][2][e], s[r][3][e]));
+                    grow = grow || (mx[r][e] - m[r][e]) * mul[r][e] > kSlack;
                 }
             if (__any_sync(0xffffffffu, grow)) {
+                const float fe = pow2i(ev - en);
+                ev = en;
 #pragma unroll
                 for (int r = 0; r < NT; r++)
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1)
-                            cand[r][e] = fmaxf(cand[r][e], __shfl_xor_sync(0xffffffffu, cand[r][e], off));
-                        const float mn = fmaxf(m[r][e], cand[r][e]), f = ex2(m[r][e] - mn);
+                            mx[r][e] = fmaxf(mx[r][e], __shfl_xor_sync(0xffffffffu, mx[r][e], off));
+                        const float mn = fmaxf(m[r][e], mx[r][e]), f = ex2((m[r][e] - mn) * mul[r][e]);
                         m[r][e] = mn;
                         l[r][e] *= f;
 #pragma unroll
                         for (int i = 0; i < 2 * NB; i++) {
-                            acc[r][i][e] *= f;
-                            acc[r][i][e + 2] *= f;
+                            acc[r][i][e] *= f * fe;
+                            acc[r][i][e + 2] *= f * fe;
                         }
                     }
             }
@@ -733,7 +748,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             for (int r = 0; r < NT; r++)
 #pragma unroll
                 for (int p = 0; p < 4; p++) {
-                    fma2(s[r][p], mul[r][0], mul[r][1], -m[r][0], -m[r][1]);
+                    sub2(s[r][p], m[r]);
+                    mul2(s[r][p], mul[r]);
                     s[r][p][0] = ex2(s[r][p][0]);
                     s[r][p][1] = ex2(s[r][p][1]);
                     add2(l[r], s[r][p]);
@@ -790,12 +806,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 for (int off = 4; off < 32; off <<= 1)
                     l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], off);
         const bool before = st0 > 0, after = t0 < snu * kUnit;
+        const float unscale = pow2i(ev - kBase);
         if (!before && !after) {
 #pragma unroll
             for (int r = 0; r < NT; r++) {
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    const float fi = l[r][c] > 0.0f ? 1.0f / l[r][c] : 0.0f;
+                    const float fi = l[r][c] > 0.0f ? unscale / l[r][c] : 0.0f;
                     const int row = row_base + 8 * r + 2 * t4 + c;
                     if (row < a.R) {
                         O *o = static_cast<O *>(a.o) +
@@ -822,13 +839,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                     float *o = pp + (8 * r + 2 * t4 + c) * C::kLd;
 #pragma unroll
                     for (int j = 0; j < NB; j++) {
-                        *reinterpret_cast<float2 *>(o + 32 * j + 2 * g) = make_float2(acc[r][2 * j][c], acc[r][2 * j + 1][c]);
-                        *reinterpret_cast<float2 *>(o + 32 * j + 16 + 2 * g) = make_float2(acc[r][2 * j][c + 2], acc[r][2 * j + 1][c + 2]);
+                        *reinterpret_cast<float2 *>(o + 32 * j + 2 * g) = make_float2(acc[r][2 * j][c] * unscale, acc[r][2 * j + 1][c] * unscale);
+                        *reinterpret_cast<float2 *>(o + 32 * j + 16 + 2 * g) = make_float2(acc[r][2 * j][c + 2] * unscale, acc[r][2 * j + 1][c + 2] * unscale);
                     }
                 }
-                if (g == 0)
+                if (g == 0) {                         // (m as q K[t]: mul is |scale2| times a power of two)
+                    const float f0 = __int_as_float(__float_as_int(mul[r][0]) - __float_as_int(fabsf(a.scale2)) + __float_as_int(1.0f));
+                    const float f1 = __int_as_float(__float_as_int(mul[r][1]) - __float_as_int(fabsf(a.scale2)) + __float_as_int(1.0f));
                     *reinterpret_cast<float4 *>(pp + C::kRows * C::kLd + 2 * (8 * r + 2 * t4)) =
-                        make_float4(m[r][0], l[r][0], m[r][1], l[r][1]);
+                        make_float4(m[r][0] * f0, l[r][0], m[r][1] * f1, l[r][1]);
+                }
             }
         }
         // the next segment
@@ -896,7 +916,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             const float *pp = w == wa ? pa : pf + w * step;
             const float2 s2 = *reinterpret_cast<const float2 *>(pp + ml);
             const float4 v = *reinterpret_cast<const float4 *>(pp + row * C::kLd + d);
-            const float f = ex2(s2.x - M);
+            const float f = ex2((s2.x - M) * fabsf(a.scale2));
             L = fmaf(f, s2.y, L);
             o.x = fmaf(f, v.x, o.x);
             o.y = fmaf(f, v.y, o.y);
@@ -967,16 +987,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll 1
             for (int it = threadIdx.x; it < nr * (D / 2); it += C::kThreads) {
                 const int row = it / (D / 2), d = it % (D / 2) * 2;
-                float M = kFloor, L = 0.0f;
+                float M = sml[row].x, L = 0.0f;
                 float2 o = make_float2(0.f, 0.f);
 #pragma unroll 4
-                for (int p = 0; p < P; p++)
+                for (int p = 1; p < P; p++)
                     M = fmaxf(M, sml[p * nr2 + row].x);
 #pragma unroll 4
                 for (int p = 0; p < P; p++) {
                     const float2 s2 = sml[p * nr2 + row];
                     const float2 v = *reinterpret_cast<const float2 *>(so + (p * nr + row) * D + d);
-                    const float f = ex2(s2.x - M);
+                    const float f = ex2((s2.x - M) * fabsf(a.scale2));
                     L = fmaf(f, s2.y, L);
                     o.x = fmaf(f, v.x, o.x);
                     o.y = fmaf(f, v.y, o.y);
@@ -1064,7 +1084,7 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     if (!kv || !kv->k_codes || !kv->k_scales || !kv->v_codes || !kv->v_scales || !q || !lens || !o || !ws)
         return BQ_ERR_NULL;
     const size_t need = bq_attn_q4_workspace_bytes(kv->D, Tq, G);
-    // (|scale| <= 1e18 keeps scale log2(e) 2^26 and every score finite)
+    // (|scale| <= 1e18 keeps scale log2(e) 2^2 finite)
     if (need == 0 || kv->Tmax < 32 || kv->Tmax % 32 != 0 || Hkv < 1 || !(std::fabs(scale) <= 1e18f) ||
         (o_dtype != BQ_F32 && o_dtype != BQ_F16))
         return BQ_ERR_SHAPE;
@@ -1102,7 +1122,7 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
     a.Tmax = kv->Tmax;
     a.R = R;
     a.passes = passes;
-    a.scale2 = scale * 1.4426950408889634f;
+    a.scale2 = std::copysign(std::fmax(std::fabs(scale) * 1.4426950408889634f, aq::kScaleMin), scale);
     a.counters = static_cast<int *>(ws);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + aq::kMaxGrid * sizeof(int));
     const int grid = sms < aq::kMaxGrid ? sms : aq::kMaxGrid;

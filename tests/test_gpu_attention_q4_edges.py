@@ -1,10 +1,10 @@
 """Decode attention over a Q4 KV cache (bq_attn_decode_q4) where its rounding,
-its reference and its masks can go wrong: fp16 output against fp32 output, the
-same contents in caches of other sizes."""
+its maximum and its masks can go wrong: fp16 output against fp32 output, the
+same contents in caches of other sizes, scores of any size."""
 import numpy as np
 import pytest
 
-from tests.kv_helpers import random_cache_q4, run_attention
+from tests.kv_helpers import attention_ref, check_attention, random_cache_q4, run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,51 @@ def test_the_same_contents_in_a_larger_cache_give_the_same_bits(Tq):
             planes.append(w)
         qq = np.concatenate([q] + [np.zeros_like(q)] * (B - 1))
         assert np.array_equal(run_attention(planes, qq, [n] + [0] * (B - 1), G, 0.088)[:1], want)
+
+
+def exact_scores(seed, B, Tq, Hkv, G, D, Tmax, dims):
+    """A cache and queries whose scores are sums of two terms, exact in fp32:
+    sum over (element, size) of dims of size * code[element], codes random and
+    scales 1; query rows differ in sign."""
+    kc, ks, vc, vs = [p.copy() for p in random_cache_q4(seed, B, Hkv, Tmax, D)]
+    r = np.random.default_rng(seed + 1)
+    kc[:] = 0x88                                                      # code 0
+    ks[:] = 0x3c00
+    q = np.zeros((B, Tq, Hkv * G, D), np.float16)
+    for d, size in dims:
+        byte = d // 32 * 16 + d % 16
+        assert d % 32 < 16                                            # (a low nibble)
+        kc[..., byte] = 0x80 | (8 + (r.integers(-8, 8, kc.shape[:3]) if size else 0))
+        q[..., d] = size
+    q[:, :, 1::2] *= -1
+    return (kc, ks, vc, vs), q.view(np.uint16)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dims,scale", [
+    # sizes of the terms of a score, softmax scale: the largest scores are ties of
+    # positions whose codes agree, others are further away than exp reaches
+    ([(3, 1024.0)], 2.0 ** 14), ([(3, 1024.0)], 2.0 ** 20), ([(3, 2.0 ** -24)], 1e18), ([(3, 32768.0)], 1e18),
+    ([(3, 32768.0)], -1e18), ([(3, 4096.0), (37, 2.0 ** -8)], 2.0 ** 14),
+    # scores of 2^25 whose differences reach into the softmax
+    ([(3, 4096.0), (37, 2.0 ** -8)], 2.0 ** 8 * 3),
+    # scores too small to matter
+    ([(3, 1.0)], 1e-30), ([(3, 32768.0)], 0.0),
+])
+@pytest.mark.parametrize("B,Tq,Hkv,G,D,Tmax,lens", [
+    (2, 1, 2, 4, 128, 512, [512, 33]),
+    (1, 1, 2, 3, 64, 8192, [8100]),
+    (2, 4, 1, 4, 128, 1024, [1000, 3]),
+    (20, 1, 8, 2, 64, 2048, [2048 - 10 * i for i in range(20)]),
+])
+def test_scores_of_any_size(B, Tq, Hkv, G, D, Tmax, lens, dims, scale, f16):
+    """The scores are exact, so check_attention's bound holds without the
+    scores' own error.  What is left of it: the exponent's argument x, an exact
+    difference of scores times scale * log2(e), takes three roundings, so that a
+    weight is off by 2^-22 x of itself: 2^-17 up to x = 2^5 (twice, for the sum of
+    weights); further weights are below 2^-32, and n <= 2^13 of them are off by
+    2^13 2^-32 2^-15 times a value below 8."""
+    planes, q = exact_scores(50, B, Tq, Hkv, G, D, Tmax, dims)
+    o_ref, ao, slack, floor = attention_ref(planes, q, lens, G, scale)
+    got = run_attention(planes, q, lens, G, scale, f16)
+    check_attention(got, (o_ref, ao, np.full_like(slack, 2 * 2.0 ** -17), floor + 2.0 ** -31), f16)
