@@ -72,6 +72,7 @@ constexpr int kWhole = 12;                // and units up to which segments are 
 constexpr int kSnap = 48;                 // segments up to this length are never cut between CTAs (see below)
 constexpr int kEdge = 1;                  // units that a segment's start counts for when the line is cut
 constexpr float kFloor = -5.0e37f;        // a maximum no score has reached (times 4 finite; times any scale a long way down)
+constexpr float kAllInf = -1.0e20f;       // in partials: every score seen is -inf (above each kFloor, below any score)
 constexpr float kSlack = 4.0f;
 constexpr int kBase = 25;                 // scales enter times 2^(25 - exponent bits): below 2^11
 constexpr float kScaleMin = 1.0e-28f;     // softmax scales below leave every score below 2^-49
@@ -812,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             for (int r = 0; r < NT; r++) {
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    const float fi = l[r][c] > 0.0f ? unscale / l[r][c] : 0.0f;
+                    const float fi = lim[r][c] > 0 ? unscale / l[r][c] : 0.0f;   // (l = 0 where every score is -inf: 0 / 0)
                     const int row = row_base + 8 * r + 2 * t4 + c;
                     if (row < a.R) {
                         O *o = static_cast<O *>(a.o) +
@@ -846,8 +847,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                 if (g == 0) {                         // (m as q K[t]: mul is |scale2| times a power of two)
                     const float f0 = __int_as_float(__float_as_int(mul[r][0]) - __float_as_int(fabsf(a.scale2)) + __float_as_int(1.0f));
                     const float f1 = __int_as_float(__float_as_int(mul[r][1]) - __float_as_int(fabsf(a.scale2)) + __float_as_int(1.0f));
-                    *reinterpret_cast<float4 *>(pp + C::kRows * C::kLd + 2 * (8 * r + 2 * t4)) =
-                        make_float4(m[r][0] * f0, l[r][0], m[r][1] * f1, l[r][1]);
+                    const float m0 = m[r][0] == kFloor && lim[r][0] > st0 * kUnit ? kAllInf : m[r][0] * f0;
+                    const float m1 = m[r][1] == kFloor && lim[r][1] > st0 * kUnit ? kAllInf : m[r][1] * f1;
+                    *reinterpret_cast<float4 *>(pp + C::kRows * C::kLd + 2 * (8 * r + 2 * t4)) = make_float4(m0, l[r][0], m1, l[r][1]);
                 }
             }
         }
@@ -924,7 +926,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             o.w = fmaf(f, v.w, o.w);
         }
         if (e.first >= plan.r0 && e.first + e.units <= plan.r1) {
-            store4(out_row(e, row) + d, o, L > 0.0f ? 1.0f / L : 0.0f);
+            store4(out_row(e, row) + d, o, M >= kAllInf ? 1.0f / L : 0.0f);
         } else {
             float *gpart = a.partials + ((size_t)cta * 2 + (e.first < plan.r0 ? 0 : 1)) * gp;
             __stcg(reinterpret_cast<float4 *>(gpart + (size_t)row * D + d), o);
@@ -1001,7 +1003,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                     o.x = fmaf(f, v.x, o.x);
                     o.y = fmaf(f, v.y, o.y);
                 }
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                const float inv = M >= kAllInf ? 1.0f / L : 0.0f;
                 store2(out_row(e, row0 + row) + d, o.x * inv, o.y * inv);
             }
             const int busy = (nr * (D / 2) + 31) / 32, from = busy < W ? busy : 0;

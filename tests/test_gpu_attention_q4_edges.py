@@ -1,6 +1,7 @@
 """Decode attention over a Q4 KV cache (bq_attn_decode_q4) where its rounding,
 its maximum and its masks can go wrong: fp16 output against fp32 output, the
-same contents in caches of other sizes, scores of any size."""
+same contents in caches of other sizes, scores of any size, scores that are all
+-inf."""
 import numpy as np
 import pytest
 
@@ -95,3 +96,26 @@ def test_scores_of_any_size(B, Tq, Hkv, G, D, Tmax, lens, dims, scale, f16):
     o_ref, ao, slack, floor = attention_ref(planes, q, lens, G, scale)
     got = run_attention(planes, q, lens, G, scale, f16)
     check_attention(got, (o_ref, ao, np.full_like(slack, 2 * 2.0 ** -17), floor + 2.0 ** -31), f16)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("B,Tq,Hkv,G,D,Tmax,lens", [
+    (2, 1, 2, 3, 128, 64, [1, 64]),                                   # whole segments
+    (1, 1, 1, 4, 64, 8192, [8000]),                                   # merged over warps and CTAs
+    (2, 5, 1, 4, 128, 1024, [1000, 3]),
+])
+def test_scores_that_are_all_minus_infinity(B, Tq, Hkv, G, D, Tmax, lens, f16):
+    """A query element of infinity against codes of one sign: every score is
+    -inf, whose softmax is NaN; a row that sees no position is 0, and rows
+    beside it do not change."""
+    planes, q = exact_scores(52, B, Tq, Hkv, G, D, Tmax, [(3, 1.0), (37, 1.0)])
+    planes[0][...] = planes[0] & 0x77 | 0x11                          # codes -7, -5, -3, -1
+    o_ref, ao, slack, floor = attention_ref(planes, q, lens, G, 0.25)
+    q[:, :, 0] = 0x7c00
+    o = run_attention(planes, q, lens, G, 0.25, f16)
+    for b in range(B):
+        for i in range(Tq):
+            sees = lens[b] - (Tq - 1 - i) > 0
+            assert np.isnan(o[b, i, 0]).all() if sees else not o[b, i, 0].any()
+    o[:, :, 0] = o_ref[:, :, 0]
+    check_attention(o, (o_ref, ao, np.full_like(slack, 2 * 2.0 ** -17), floor + 2.0 ** -31), f16)
