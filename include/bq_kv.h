@@ -126,8 +126,10 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *   q       device fp16 bits [B][Tq][Hkv*G][D]
  *   lens    device int32 [B]: valid positions of sequence b, the query tokens'
  *           included (clamped to [0, Tmax]).  A query token that sees no
- *           position gets o = 0.  Nothing at or past lens[b] is read into the
- *           result, whatever the cache holds there.
+ *           position gets o = 0.  Nothing that a query token does not see is
+ *           read into its result, whatever the cache holds there.  (A value
+ *           scale that is not finite makes NaN of its block's 32 elements for
+ *           the tokens that see it, a key scale of whole rows.)
  *   Tq      query tokens a sequence, 1..32
  *   G       query heads per KV head, 1..16
  *   scale   softmax scale, |scale| <= 1e18 (any sign; below 1e-28 as 1e-28)
@@ -142,7 +144,7 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  * enter the tensor cores exactly.  Weights are made from differences of unscaled
  * scores, so scores may be of any size.  Each softmax weight times its value scale
  * enters as two fp16 terms: off by 2^-21 of it or, where that is more, by 2^-35
- * of the largest value scale (2^-14 at least) below lens[b].  BQ_F16 output is
+ * of the largest finite value scale (2^-14 at least) below lens[b].  BQ_F16 output is
  * the BQ_F32 output rounded once.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE (D, Tmax, Hkv, G, Tq, scale, o_dtype, cache
  * size; also B * Hkv * Tmax * passes >= 2^35, which Tq * G <= 256 never

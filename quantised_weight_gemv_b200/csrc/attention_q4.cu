@@ -653,8 +653,32 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
             uint32_t sc[NB / 2];
             (void)load_scales<NB>(sc, kb + 2 * C::kCodes + lane * NB * 2, valid);
             store_scales<NB>(conv + lane * NB * 4, sc, 1.0f);
-            const int top = (int)__reduce_max_sync(
+            int top = (int)__reduce_max_sync(
                 0xffffffffu, load_scales<NB>(sc, kb + 2 * C::kCodes + C::kScales + lane * NB * 2, valid)) >> 10;
+            if (top == 31) {
+                // Value scales that are not finite: they enter as 0, so that weights of 0
+                // past a row's end stay 0, and the blocks of the rows that see one are NaN.
+                uint32_t mx = 0;
+#pragma unroll
+                for (int j = 0; j < NB; j++) {
+                    const uint32_t h = sc[j >> 1] >> 16 * (j & 1) & 0x7fffu;
+                    const unsigned bad = __ballot_sync(0xffffffffu, h >= 0x7c00u);
+                    if (h >= 0x7c00u)
+                        sc[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+                    else
+                        mx = max(mx, h);
+#pragma unroll
+                    for (int r = 0; r < NT; r++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int n = lim[r][e] - t0;         // positions of the unit that the row sees
+                            if (n > 0 && bad & (n < kUnit ? (1u << n) - 1u : ~0u))
+                                acc[r][2 * j][e] = acc[r][2 * j][e + 2] = acc[r][2 * j + 1][e] = acc[r][2 * j + 1][e + 2] =
+                                    __int_as_float(0x7fffffff);
+                        }
+                }
+                top = (int)__reduce_max_sync(0xffffffffu, mx) >> 10;
+            }
             const int en = max(ev, top);
             store_scales<NB>(conv + (kUnit + lane) * NB * 4, sc, pow2i(kBase - en));
             __syncwarp();

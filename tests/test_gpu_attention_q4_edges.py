@@ -1,7 +1,7 @@
 """Decode attention over a Q4 KV cache (bq_attn_decode_q4) where its rounding,
 its maximum and its masks can go wrong: fp16 output against fp32 output, the
 same contents in caches of other sizes, scores of any size, scores that are all
--inf."""
+-inf, value scales that are not finite where some rows do not see them."""
 import numpy as np
 import pytest
 
@@ -119,3 +119,29 @@ def test_scores_that_are_all_minus_infinity(B, Tq, Hkv, G, D, Tmax, lens, f16):
             assert np.isnan(o[b, i, 0]).all() if sees else not o[b, i, 0].any()
     o[:, :, 0] = o_ref[:, :, 0]
     check_attention(o, (o_ref, ao, np.full_like(slack, 2 * 2.0 ** -17), floor + 2.0 ** -31), f16)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("Tq,G,D,n", [(1, 4, 128, 70), (2, 4, 128, 65), (4, 2, 64, 33), (8, 5, 128, 300), (8, 4, 64, 64),
+                                      (32, 2, 128, 97), (5, 3, 128, 4100), (3, 8, 128, 40)])
+def test_value_scales_that_are_not_finite_stay_with_the_rows_that_see_them(Tq, G, D, n, f16):
+    """NaN and infinite value scales at the last positions: a query token that
+    does not see one is as accurate as without it, one that does is NaN in that
+    block's 32 elements alone."""
+    Hkv, Tmax, scale = 2, -(-n // 32) * 32, D ** -0.5
+    planes = [p.copy() for p in random_cache_q4(54, 1, Hkv, Tmax, D)]
+    q = q_bits(55, 1, Tq, Hkv * G, D)
+    bad = [(n - 1, 0, 0x7e00), (n - 1, 1, 0x7c00), (n - 2, 1, 0xfc00), (n - Tq // 2 - 1, 0, 0x7c00), (n - Tq, D // 32 - 1, 0xfe00)]
+    for t, j, bits in bad:
+        planes[3][:, :, t, j] = 0                                     # (the reference: without them)
+    o_ref, ao, slack, floor = attention_ref(planes, q, [n], G, scale)
+    for t, j, bits in bad:
+        planes[3][:, :, t, j] = bits
+    o = run_attention(planes, q, [n], G, scale, f16)
+    for i in range(Tq):
+        nan = np.zeros(D, bool)
+        for t, j, _ in bad:
+            nan[32 * j:32 * j + 32] |= t < n - (Tq - 1 - i)
+        assert np.isnan(o[0, i][:, nan]).all()
+        o[0, i][:, nan] = o_ref[0, i][:, nan]
+    check_attention(o, (o_ref, ao, slack, floor), f16)
