@@ -81,7 +81,8 @@ typedef struct bq_kv_rows {
  *   rows    source rows (read only)
  *   B, Hkv  sequences and KV heads of the cache and of the rows; Hkv <= 65535
  *   start   device int32 [B]: first position written
- *   count   device int32 [B], or NULL: every sequence writes T rows
+ *   count   device int32 [B], or NULL: every sequence writes T rows.  Rows from
+ *           count[b] on are not read, nor are those past the cache's end
  * Device status: BQ_ERR_POSITION for rows whose position is outside [0, Tmax)
  * (those are not written) and for counts outside [0, T] (taken as the nearer
  * end); BQ_ERR_RANGE for a 32-block that is not finite or whose scale overflows

@@ -1,0 +1,63 @@
+"""Writing the KV caches at the edges of what a call names: rows from a
+sequence's count on."""
+import numpy as np
+import pytest
+
+from quantised_weight_gemv_b200 import bq
+from tests.gpu_helpers import DEV
+from tests.test_gpu_kv_cache import dtype, ints, make_kv, new_cache, place, planes_of, rows, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("src", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("fmt,B,T,Hkv,D,Tmax,start,count", [
+    (4, 4, 40, 3, 128, 64, [0, 20, 3, 63], [0, 1, 33, 1]),
+    (4, 3, 70, 2, 64, 128, [5, 0, 60], [17, 64, 3]),
+    # four rows a thread: counts at, one short of and one past a block's and a warp's rows
+    (4, 8, 1400, 5, 128, 1408, [0, 1, 0, 3, 0, 0, 5, 8], [0, 1, 16, 17, 63, 64, 65, 1400]),
+    (4, 6, 2600, 5, 64, 2624, [0, 7, 0, 0, 24, 0], [1, 127, 128, 129, 2600, 0]),
+    (8, 4, 300, 2, 128, 384, [0, 77, 3, 84], [0, 1, 129, 300]),
+])
+def test_rows_from_the_count_on_do_not_matter(fmt, B, T, Hkv, D, Tmax, start, count, src):
+    """They hold NaN: nothing of them is stored or reported."""
+    planes = new_cache(fmt, B, Hkv, Tmax, D)
+    kv = make_kv(fmt, planes)
+    k, v, kf, vf = rows(60 + T, B, T, Hkv, D, src)
+    k, v = k.clone(), v.clone()
+    for b, n in enumerate(count):
+        k[b, n:], v[b, n:] = float("nan"), float("nan")
+    st = status()
+    bq.kv_append(kv, k, v, ints(start), ints(count), st)
+    assert int(st.item()) == 0
+    for got, w in zip(planes_of(kv), place(fmt, planes, kf, vf, start, count)):
+        assert np.array_equal(got, w)
+
+
+@pytest.mark.parametrize("src", ["f32", "f16"])
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_rows_from_the_count_on_are_not_read(fmt, src):
+    """Seen by the time: 16 sequences of 4096 rows, 0.27 or 0.54 GB, with a count
+    of 1 each take less than half of what all rows take, where reading them all
+    takes as long."""
+    import torch
+    B, T, H, D = 16, 4096, 8, 128
+    kv = make_kv(fmt, new_cache(fmt, B, H, T, D, fill=0))
+    x = torch.randn((B, T, 2 * H, D), device=DEV).to(dtype(src))
+    start = ints([0] * B)
+
+    def us(count):
+        best = float("inf")
+        for _ in range(8):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            for _ in range(4):                        # (4 launches: the device, not the host's calls)
+                bq.kv_append(kv, x[:, :, :H], x[:, :, H:], start, count)
+            e[1].record()
+            torch.cuda.synchronize()
+            best = min(best, e[0].elapsed_time(e[1]) * 250)
+        return best
+
+    us(None)
+    every, few = us(None), us(ints([1] * B))
+    assert few < every / 2, (few, every)
