@@ -550,11 +550,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
                        (lane < kSc ? a.ks : a.vs) + (size_t)(unsigned)is_row * NB + (lane & (kSc - 1)) * 8);
             to_issue--;
             is_row += kUnit;
-            if (--is_left == 0) {
+            // (only where there is more to copy: behind the last sequence lie idle slots, and each is a load to wait for)
+            if (--is_left == 0 && (to_issue -= edge) > 0) {
                 Cursor c = copy_at[warp];
                 if (++c.hp == HP)
                     next_seq(c);
-                to_issue -= edge;
                 is_left = c.nu;
                 is_row = seg_row(c);
                 __syncwarp();
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) attn_q4_kernel(const 
         cur.t = 0;
         if (!after) {
             u += edge;
-            if (++cur.hp == HP)
+            if (u < w1 && ++cur.hp == HP)
                 next_seq(cur);
         }
     }

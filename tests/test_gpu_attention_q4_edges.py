@@ -1,11 +1,14 @@
 """Decode attention over a Q4 KV cache (bq_attn_decode_q4) where its rounding,
 its maximum and its masks can go wrong: fp16 output against fp32 output, the
 same contents in caches of other sizes, scores of any size, scores that are all
--inf, value scales that are not finite where some rows do not see them."""
+-inf, value scales that are not finite where some rows do not see them,
+idle slots."""
 import numpy as np
 import pytest
 
-from tests.kv_helpers import attention_ref, check_attention, random_cache_q4, run_attention
+from quantised_weight_gemv_b200 import bq
+from tests.gpu_helpers import DEV
+from tests.kv_helpers import attention_ref, check_attention, random_cache_q4, run_attention, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +148,55 @@ def test_value_scales_that_are_not_finite_stay_with_the_rows_that_see_them(Tq, G
         assert np.isnan(o[0, i][:, nan]).all()
         o[0, i][:, nan] = o_ref[0, i][:, nan]
     check_attention(o, (o_ref, ao, slack, floor), f16)
+
+
+@pytest.mark.parametrize("where", ["first", "last", "apart"])
+@pytest.mark.parametrize("n", [1, 8])
+def test_idle_slots_beside_live_sequences(where, n):
+    """1000 slots, n of them live: the live ones' rows against fp64, the others 0."""
+    B, Hkv, G, D, Tmax = 1000, 2, 3, 64, 512
+    at = {"first": range(n), "last": range(B - n, B), "apart": range(3, B, B // n)}[where]
+    part = random_cache_q4(56, n, Hkv, Tmax, D)
+    planes = []
+    for p in part:
+        w = np.zeros((B, *p.shape[1:]), p.dtype)
+        w[list(at)] = p
+        planes.append(w)
+    lens, live = np.zeros(B, np.int32), [512 - 37 * i for i in range(n)]
+    lens[list(at)] = live
+    q = q_bits(57, B, 1, Hkv * G, D)
+    o = run_attention(planes, q, lens, G, 0.125)
+    check_attention(o[list(at)], attention_ref(part, q[list(at)], live, G, 0.125), True)
+    o[list(at)] = 0
+    assert not o.any()
+
+
+def test_idle_slots_behind_the_live_ones_are_not_walked():
+    """Seen by the time: 8 sequences at the front of 1000 slots take less than
+    twice as long as at the back, where a walk over the idle slots behind them, a
+    load after another, takes five times as long."""
+    import torch
+    B, Hkv, G, D, Tmax = 1000, 8, 5, 128, 4096
+    planes = [torch.zeros((B, Hkv, Tmax, D // n), dtype=t, device=DEV) for n, t in ((2, torch.uint8), (32, torch.int16)) * 2]
+    kv = bq.kv_cache_q4(*planes)
+    q = to_dev(q_bits(58, B, Hkv * G, D))
+    o = torch.zeros((B, Hkv * G, D), device=DEV)
+    ws = bq.workspace(bq.lib().bq_attn_q4_workspace_bytes(D, 1, G), DEV)
+
+    def us(first):
+        lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+        lens[first:first + 8] = Tmax
+        best = float("inf")
+        for _ in range(8):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            for _ in range(8):                        # (8 launches: the device, not the host's calls)
+                bq.attn_decode_q4(kv, q, lens, G, 0.09, o, ws)
+            e[1].record()
+            torch.cuda.synchronize()
+            best = min(best, e[0].elapsed_time(e[1]) * 125)
+        return best
+
+    us(0)
+    front, back = us(0), us(B - 8)
+    assert front < 2 * back, (front, back)
