@@ -69,7 +69,7 @@ constexpr int kUnit = 32;                 // positions per unit
 constexpr int kMaxGrid = 160;             // CTAs (one per SM)
 constexpr int kMinUnits[2] = {4, 8};      // units per CTA of 16 or 8 warps, where there are few,
 constexpr int kWhole = 12;                // and units up to which segments are whole then (see make_plan)
-constexpr int kSnap = 48;                 // segments up to this length are never cut between CTAs (see below)
+constexpr int kSnap = 32;                 // segments up to this length are never cut between CTAs (see below)
 constexpr int kEdge = 1;                  // units that a segment's start counts for when the line is cut
 constexpr float kFloor = -5.0e37f;        // a maximum no score has reached (times 4 finite; times any scale a long way down)
 constexpr float kAllInf = -1.0e20f;       // in partials: every score seen is -inf (above each kFloor, below any score)
@@ -314,8 +314,12 @@ __device__ __forceinline__ void each_own(const Args &a, const int (&own)[PER ? P
 // read and scaled, outputs written) counts as kEdge units, laid before its
 // first: without that a warp whose share was 14 segments of two units held up
 // the others (256 sequences of 1 to 2048 positions, 8 KV heads: 87 us, so 73;
-// 64 of 1 to 4096: 54 and 43).  A cut inside a short segment moves to its nearer
-// end: 24 units more at most, against a merge across CTAs.
+// 64 of 1 to 4096: 54 and 43).  A cut inside a segment of up to kSnap units moves
+// to its nearer end.  A share has two cuts, so it may grow by kSnap units, against
+// merges across CTAs: 152 segments of 32 units, whose largest share is then 66 and
+// not 34, take 17.4 us, cut evenly 18.4; 64 x 8 of up to 32 units at D = 64 13.9 and
+// 16.6; but 152 segments of 48 units, with shares of up to 98 and not 51, 22.9, cut
+// evenly 21.8.
 //
 // Few units: where no segment has more than 12, each keeps one CTA (8 segments of
 // 12 units 7.5 us; split 8.5); else a CTA of 16 warps takes 4 at least (8 segments

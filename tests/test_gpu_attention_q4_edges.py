@@ -2,7 +2,7 @@
 its maximum and its masks can go wrong: fp16 output against fp32 output, the
 same contents in caches of other sizes, scores of any size, scores that are all
 -inf, value scales that are not finite where some rows do not see them,
-idle slots."""
+idle slots, numbers of segments just above the grid."""
 import numpy as np
 import pytest
 
@@ -200,3 +200,15 @@ def test_idle_slots_behind_the_live_ones_are_not_walked():
     us(0)
     front, back = us(0), us(B - 8)
     assert front < 2 * back, (front, back)
+
+
+@pytest.mark.parametrize("B,Hkv,Tmax,lens", [
+    # segments of 48, 33, 32 and 31 units, two cuts beside one, long ones between short ones
+    (19, 8, 1536, [1536] * 19), (19, 8, 1056, [1056] * 19), (19, 8, 1024, [1024] * 19), (38, 4, 992, [992 - i for i in range(38)]),
+    (24, 8, 1088, [960 + (37 * i) % 129 for i in range(24)]), (40, 4, 4096, [4096 if i % 10 == 3 else 300 + 40 * i for i in range(40)]),
+])
+def test_numbers_of_segments_just_above_the_grid(B, Hkv, Tmax, lens):
+    planes = random_cache_q4(59, B, Hkv, Tmax, 64)
+    q = q_bits(60, B, 1, Hkv, 64)
+    o = run_attention(planes, q, lens, 1, 0.125, False)
+    check_attention(o, attention_ref(planes, q, lens, 1, 0.125), False)
