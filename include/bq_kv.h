@@ -101,7 +101,8 @@ BQ_API int32_t bq_kv_append_q8(const bq_kv_cache *kv, const bq_kv_rows *rows, in
  * and rounded once (to nearest even) to fp16 or bf16.  A magnitude above
  * fp16's range becomes infinite.  Rows from count[b] on, and rows of positions
  * outside [0, Tmax), are left as they were.
- *   rows    destination; k or v (not both) may be NULL and is then skipped
+ *   rows    destination; k or v (not both) may be NULL and is then skipped; k
+ *           and v at one address are refused (BQ_ERR_SHAPE)
  * Other arguments, device status (BQ_ERR_POSITION) and errors as
  * bq_kv_append_*. */
 BQ_API int32_t bq_kv_read_q4(const bq_kv_cache_q4 *kv, const bq_kv_rows *rows, int32_t B,

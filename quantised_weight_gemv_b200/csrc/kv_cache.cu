@@ -718,6 +718,8 @@ int32_t run_q4(Op op, const bq_kv_cache_q4 *kv, const bq_kv_rows *rows, int32_t 
         return st;
     if (!aligned16(kv->k_codes) || !aligned16(kv->k_scales) || !aligned16(kv->v_codes) || !aligned16(kv->v_scales))
         return BQ_ERR_ALIGN;
+    if (op == kRead && rows->k == rows->v)                // (two writers of the same rows)
+        return BQ_ERR_SHAPE;
     a.kc = kv->k_codes;
     a.vc = kv->v_codes;
     a.ks = kv->k_scales;
@@ -752,6 +754,8 @@ int32_t run_q8(Op op, const bq_kv_cache *kv, const bq_kv_rows *rows, int32_t B, 
         return st;
     if (!aligned16(kv->k_codes) || !aligned16(kv->k_scales) || !aligned16(kv->vt_codes) || !aligned16(kv->v_scales))
         return BQ_ERR_ALIGN;
+    if (op == kRead && rows->k == rows->v)
+        return BQ_ERR_SHAPE;
     a.kc = reinterpret_cast<uint8_t *>(const_cast<int8_t *>(kv->k_codes));
     a.vc = reinterpret_cast<uint8_t *>(const_cast<int8_t *>(kv->vt_codes));
     a.ks = const_cast<uint16_t *>(kv->k_scales);

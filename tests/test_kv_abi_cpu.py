@@ -200,3 +200,10 @@ def test_overlap_rule():
     ov = bq._overlaps
     assert not ov((2, 3, 4), (12, 4, 1)) and not ov((1, 3, 4), (0, 4, 1)) and not ov((3, 2, 4), (4, 12, 1))
     assert ov((2, 3, 4), (0, 4, 1)) and ov((2, 4), (3, 1)) and not ov((2, 4), (4, 1))
+
+
+@pytest.mark.parametrize("fn", ["bq_kv_read_q4", "bq_kv_read_q8"])
+def test_a_read_into_one_buffer_is_refused(fn):
+    """k and v at one address, where keys and values would overwrite each other."""
+    for dtype in (0, 1, 2):
+        assert rows_rc(fn, dtype=dtype) == bq.BQ_ERR_SHAPE
