@@ -136,7 +136,8 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *   G       query heads per KV head, 1..16
  *   scale   softmax scale, |scale| <= 1e18 (any sign; below 1e-28 as 1e-28)
  *   o       device [B][Tq][Hkv*G][D], overwritten; o_dtype BQ_F32 or BQ_F16
- *           (the input type of the next bq_gemv); must not overlap q
+ *           (the input type of the next bq_gemv); must not overlap q (at q's
+ *           address: BQ_ERR_SHAPE)
  *   ws      device workspace >= bq_attn_q4_workspace_bytes(D, Tq, G),
  *           zero-filled before first use, left zero-filled by every call that
  *           completes; not shared with calls that may run at the same time

@@ -1132,6 +1132,8 @@ extern "C" int32_t bq_attn_decode_q4(const bq_kv_cache_q4 *kv, const uint16_t *q
         return BQ_ERR_ALIGN;
     if (ws_bytes < need)
         return BQ_ERR_WORKSPACE;
+    if (o == q)
+        return BQ_ERR_SHAPE;
     (void)dev_status;                                 // nothing here can fail on the device
     const int sms = device_sm_count();
     if (sms <= 0)

@@ -207,3 +207,7 @@ def test_a_read_into_one_buffer_is_refused(fn):
     """k and v at one address, where keys and values would overwrite each other."""
     for dtype in (0, 1, 2):
         assert rows_rc(fn, dtype=dtype) == bq.BQ_ERR_SHAPE
+
+
+def test_an_attention_output_over_its_queries_is_refused():
+    assert attn_rc(od=1) == attn_rc(od=0) == bq.BQ_ERR_SHAPE
