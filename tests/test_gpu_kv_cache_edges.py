@@ -1,10 +1,12 @@
-"""Writing the KV caches at the edges of what a call names: rows from a
-sequence's count on."""
+"""Writing and reading the KV caches at the edges of what a call names: rows from
+a sequence's count on, offsets past 32 bits in the Q8 cache and in rows."""
 import numpy as np
 import pytest
 
+import oracle
 from quantised_weight_gemv_b200 import bq
 from tests.gpu_helpers import DEV
+from tests.kv_helpers import quant_rows
 from tests.test_gpu_kv_cache import dtype, ints, make_kv, new_cache, place, planes_of, rows, status
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +63,50 @@ def test_rows_from_the_count_on_are_not_read(fmt, src):
     us(None)
     every, few = us(None), us(ints([1] * B))
     assert few < every / 2, (few, every)
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_q8_cache_offsets_past_32_bits(T):
+    """A Q8 cache whose third sequence starts 2^32 bytes into the code planes."""
+    import torch
+    B, H, Tmax, D = 3, 1, 1 << 24, 128
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of free device memory")
+    refs = [torch.empty(s, dtype=t, device=DEV) for s, t in
+            (((B, H, Tmax, D), torch.int8), ((B, H, Tmax, D // 32), torch.int16),
+             ((B, H, D, Tmax), torch.int8), ((B, H, Tmax, D // 32), torch.int16))]
+    kv = bq.kv_cache(*refs)
+    k, v, kf, vf = rows(70, B, T, H, D, "f32")
+    start = [0, 5, Tmax - T]
+    bq.kv_append(kv, k, v, ints(start))
+    ko, vo = torch.zeros((B, T, H, D), device=DEV), torch.zeros((B, T, H, D), device=DEV)
+    bq.kv_read(kv, ko, vo, ints(start))
+    for x, y in ((kf, ko), (vf, vo)):
+        c, s = quant_rows(8, x)
+        want = c.view(np.int8).astype(np.float64) * oracle.half_to_double(s).repeat(32, -1)
+        assert np.array_equal(y.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_row_offsets_past_32_bits(fmt):
+    """Source and destination rows 2^32 elements apart (8.6 GB of fp16)."""
+    import torch
+    D, far = 128, 1 << 32
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of free device memory")
+    buf = torch.empty(far + 2 * D, dtype=torch.float16, device=DEV)
+    src = buf.as_strided((1, 2, 1, D), (far + 2 * D, far, D, 1))        # two tokens
+    seq = buf.as_strided((2, 1, 1, D), (far, D, D, 1))                  # two sequences
+    x = torch.from_numpy(np.random.default_rng(71).standard_normal((2, D)).astype(np.float16)).to(DEV)
+    for rows_, B in ((src, 1), (seq, 2)):
+        T = 2 // B
+        rows_.copy_(x.view(B, T, 1, D))
+        kv = make_kv(fmt, new_cache(fmt, B, 1, 128, D))
+        bq.kv_append(kv, rows_, rows_, ints([9] * B))
+        want = place(fmt, new_cache(fmt, B, 1, 128, D), *[x.float().cpu().numpy().reshape(B, T, 1, D)] * 2, [9] * B, [T] * B)
+        for got, w in zip(planes_of(kv), want):
+            assert np.array_equal(got, w)
+        rows_.zero_()
+        ko = torch.zeros((B, T, 1, D), dtype=torch.float16, device=DEV)
+        bq.kv_read(kv, ko, rows_, ints([9] * B))
+        assert torch.equal(ko, rows_) and bool((ko != 0).any(-1).all())
