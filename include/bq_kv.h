@@ -131,7 +131,7 @@ BQ_API size_t bq_attn_q4_workspace_bytes(int32_t D, int32_t Tq, int32_t G);
  *           position gets o = 0.  Nothing that a query token does not see is
  *           read into its result, whatever the cache holds there.  (A value
  *           scale that is not finite makes NaN of its block's 32 elements for
- *           the tokens that see it, a key scale of whole rows.)
+ *           the tokens that see it; a NaN key scale, of whole rows.)
  *   Tq      query tokens a sequence, 1..32
  *   G       query heads per KV head, 1..16
  *   scale   softmax scale, |scale| <= 1e18 (any sign; below 1e-28 as 1e-28)

@@ -212,3 +212,40 @@ def test_numbers_of_segments_just_above_the_grid(B, Hkv, Tmax, lens):
     q = q_bits(60, B, 1, Hkv, 64)
     o = run_attention(planes, q, lens, 1, 0.125, False)
     check_attention(o, attention_ref(planes, q, lens, 1, 0.125), False)
+
+
+@pytest.mark.parametrize("bits", [0x7e00, 0x7c00, 0xfc00])
+@pytest.mark.parametrize("Tq,G,D,n", [(2, 4, 128, 65), (8, 5, 128, 300), (4, 2, 64, 33)])
+def test_key_scales_that_are_not_finite_stay_with_the_rows_that_see_them(Tq, G, D, n, bits):
+    """The last token's own key scale: earlier tokens are as accurate as without
+    it, the last is NaN where the scale is."""
+    Hkv, Tmax, scale = 2, -(-n // 32) * 32, D ** -0.5
+    planes = [p.copy() for p in random_cache_q4(61, 1, Hkv, Tmax, D)]
+    q = q_bits(62, 1, Tq, Hkv * G, D)
+    ref = [r[:, :-1] for r in attention_ref(planes, q, [n], G, scale)]
+    planes[1][:, :, n - 1, 1] = bits
+    o = run_attention(planes, q, [n], G, scale)
+    check_attention(o[:, :-1], ref, True)
+    if bits == 0x7e00:
+        assert np.isnan(o[:, -1]).all()
+
+
+def test_more_sequences_than_a_grid_has_rows():
+    """70000 sequences, 150 of them with positions."""
+    B, Hkv, G, D, Tmax = 70000, 1, 2, 64, 32
+    r = np.random.default_rng(63)
+    at = np.sort(r.choice(B, 150, replace=False))
+    at[0], at[-1] = 0, B - 1
+    part = random_cache_q4(64, 150, Hkv, Tmax, D)
+    planes = []
+    for p in part:
+        w = np.zeros((B, *p.shape[1:]), p.dtype)
+        w[at] = p
+        planes.append(w)
+    lens, live = np.zeros(B, np.int32), r.integers(1, 33, 150)
+    lens[at] = live
+    q = q_bits(65, B, 1, Hkv * G, D)
+    o = run_attention(planes, q, lens, G, 0.125)
+    check_attention(o[at], attention_ref(part, q[at], live, G, 0.125), True)
+    o[at] = 0
+    assert not o.any()

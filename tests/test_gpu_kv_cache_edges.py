@@ -6,7 +6,7 @@ import pytest
 import oracle
 from quantised_weight_gemv_b200 import bq
 from tests.gpu_helpers import DEV
-from tests.kv_helpers import quant_rows
+from tests.kv_helpers import deq_q4, quant_rows
 from tests.test_gpu_kv_cache import dtype, ints, make_kv, new_cache, place, planes_of, rows, status
 
 pytestmark = pytest.mark.gpu
@@ -110,3 +110,25 @@ def test_row_offsets_past_32_bits(fmt):
         ko = torch.zeros((B, T, 1, D), dtype=torch.float16, device=DEV)
         bq.kv_read(kv, ko, rows_, ints([9] * B))
         assert torch.equal(ko, rows_) and bool((ko != 0).any(-1).all())
+
+
+@pytest.mark.parametrize("fmt,D,Tmax", [(4, 64, 32), (8, 128, 128)])
+def test_more_sequences_than_a_grid_has_rows(fmt, D, Tmax):
+    """70000 sequences: a token each at odd places, some with none."""
+    import torch
+    B = 70000
+    kv = make_kv(fmt, new_cache(fmt, B, 1, Tmax, D))
+    k, v, kf, vf = rows(72, B, 1, 1, D, "f16")
+    start, count = np.arange(B) * 7 % Tmax, (np.arange(B) % 5 != 2).astype(np.int32)
+    st = status()
+    bq.kv_append(kv, k, v, ints(start), ints(count), st)
+    assert int(st.item()) == 0
+    for got, w in zip(planes_of(kv), place(fmt, new_cache(fmt, B, 1, Tmax, D), kf, vf, start, count)):
+        assert np.array_equal(got, w)
+    ko, vo = torch.zeros((B, 1, 1, D), device=DEV), torch.zeros((B, 1, 1, D), device=DEV)
+    bq.kv_read(kv, ko, vo, ints(start), ints(count), st)
+    assert int(st.item()) == 0
+    for x, y in ((kf, ko), (vf, vo)):
+        c, s = quant_rows(fmt, x)
+        want = (deq_q4(c, s) if fmt == 4 else c.view(np.int8) * oracle.half_to_double(s).repeat(32, -1))
+        assert np.array_equal(y.cpu().numpy(), want * count[:, None, None, None])
