@@ -5,11 +5,12 @@
 // Bound: a position of one KV head is 144 bytes (D = 128), read once for its
 // R = Tq * G query rows: 4 D R / 144 flops a byte, so HBM up to about 16 rows;
 // what stands against it is the number of instructions that unpack 256 codes.
-// Measured in a chain of graph launches (D = 128, 8 KV heads, 5 query heads
-// each): 8 sequences of 32768 positions 75 us, 4.0 TB/s, of which 10 us are the
-// two ends (plan, first loads, merges); one of 32768 21 us; one of 4096 10 us,
-// nearly all ends.  40 rows (8 query tokens) at 8 x 3k positions on average:
-// 43 us, bound by instructions.
+// Measured in a chain of launches (D = 128, 8 KV heads, 5 query heads each): 8
+// sequences of 32768 positions 75.5 us, 4.0 TB/s, bound by instructions (719 a
+// unit of 32 positions; the copies alone 58 us); one of 32768 20 us; one of 4096
+// 10 us, nearly all ends (plan, first loads, merges).  A launch by itself takes
+// up to 6 us more, its start and end.  40 rows (8 query tokens) at 8 x 3k
+// positions on average: 43 us.
 //
 // Work: a unit is 32 positions of one (sequence, KV head).  The valid units of
 // all sequences form one line (lens are on the device: one warp of every CTA
@@ -31,8 +32,10 @@
 // are merged at the end: warps through shared memory, CTAs through the
 // workspace, where the last CTA to arrive merges in CTA order (deterministic).
 //
-// Tensor cores (mma.sync m16n8k16; with 8 or 16 rows a tcgen05 tile of 128
-// rows would be empty), fp32 accumulation, codes exact:
+// Tensor cores (mma.sync m16n8k16), fp32 accumulation, codes exact.  (Not
+// tcgen05: positions, or head elements, would fill its 128 rows, but value scales
+// differ by position and block, and 16 MMAs of 70 to 130 cycles each for 128
+// positions are no less than the 1200 cycles that these take at up to 8 rows.)
 //   scores  S^T[t][row]: A = key codes u - 8 (exact fp16: (0x6400 | u) - 1032),
 //     B = q.  Positions fill the 16-row side, so no operand is padded.  Each
 //     block's sum is scaled by dK in fp32.  q is multiplied by a power of two a
@@ -43,7 +46,7 @@
 //     two fp16 terms, whatever the output's type: one term would round every
 //     weight as coarsely as a 16-bit output is rounded, 1.4 times the error of
 //     the output's own rounding (8 x 32768 positions: 2.9e-4 of the result instead
-//     of 2.1e-4, in 61 us instead of 75).  ldmatrix.trans on 16-bit units turns
+//     of 2.1e-4, in 61 us and not 75).  ldmatrix.trans on 16-bit units turns
 //     position-major rows into pairs of positions per register.
 //   p dV reaches B's layout by one movmatrix a tile and never leaves registers.
 // Exponents: p = 2^((s - m) scale log2(e)) with s and m still unscaled sums, so
@@ -308,32 +311,31 @@ __device__ __forceinline__ void each_own(const Args &a, const int (&own)[PER ? P
 // Split: every segment has CTAs of its own, about units / T of them, if that
 // takes no more than the grid with T at most 24 units (3/16) above an even
 // share.  Otherwise the line is cut evenly, and a CTA that shares two segments
-// merges twice, 3 us more, the time of 24 units: 16.5 against 13.5 us at 8
-// segments of 256 units; but 68 us cut evenly against 73 at 64 segments of
-// 1024 units, where T would be 69 more.  On the line a segment's start (queries
-// read and scaled, outputs written) counts as kEdge units, laid before its
-// first: without that a warp whose share was 14 segments of two units held up
-// the others (256 sequences of 1 to 2048 positions, 8 KV heads: 87 us, so 73;
-// 64 of 1 to 4096: 54 and 43).  A cut inside a segment of up to kSnap units moves
+// merges twice: 64 query rows over 2 segments of 64 units 22.5 us, split 15.6; 8
+// segments of 256 units 13.5 and 13.1; but 76 us cut evenly and 83 split at 64
+// segments of 1024 units, where T would be 69 more.  On the line a segment's start
+// (queries read and scaled, outputs written) counts as kEdge units, laid before
+// its first: without that a warp whose share was 14 segments of two units held up
+// the others (256 sequences of 1 to 2048 positions, 8 KV heads: 97 us, so 83;
+// 64 of 1 to 4096: 59 and 49).  A cut inside a segment of up to kSnap units moves
 // to its nearer end.  A share has two cuts, so it may grow by kSnap units, against
 // merges across CTAs: 152 segments of 32 units, whose largest share is then 66 and
 // not 34, take 17.4 us, cut evenly 18.4; 64 x 8 of up to 32 units at D = 64 13.9 and
-// 16.6; but 152 segments of 48 units, with shares of up to 98 and not 51, 22.9, cut
-// evenly 21.8.
+// 16.6; but 152 of 48 units, with shares of up to 98 and not 51, 22.9 and 21.8.
 //
 // Few units: where no segment has more than 12, each keeps one CTA (8 segments of
-// 12 units 7.5 us; split 8.5); else a CTA of 16 warps takes 4 at least (8 segments
-// of 16 units 8.5 us; with 8 at least 9.0), one of 8 warps 8 (64 query rows over 2
-// segments of 64 units 15.4 us; with 4 at least 16.6).
+// 12 units 7.4 us; split 8.4); else a CTA of 16 warps takes 4 at least (8 segments
+// of 16 units 8.4 us; with 8 at least 8.9), one of 8 warps 8 (64 query rows over 2
+// segments of 64 units 15.6 us; with 4 at least 17.0).
 //
 // Up to 32 sequences a lane has one, up to 128 PER = 4, and the plan is
 // straight-line code on registers; beyond (PER = 0), a lane has a chunk of them,
 // and loops over it.  What this costs is fetching instructions that run once: one
-// sequence of 32768 positions took 20 us with integer divisions and loops
-// throughout, 19 without the divisions, 18 without the loops; 128 sequences of 512
-// 17.0 us with loops, 16.5 without.  (Their units laid out in shared memory first:
-// 1024 sequences of one unit 12.9 instead of 14.5 us, but all small calls 0.1 to
-// 0.2 us more for the code in between.)
+// sequence of 32768 positions takes 21.6 us with loops and 21.1 so, one of 4096
+// 10.7 and 10.2, 128 of 512 29.1 and 28.4 (the four-sequence code alone: 21.3, 10.5
+// and 28.1); integer divisions throughout took 1 us more.  (Their units laid out in
+// shared memory first: 1024 sequences of one unit 1.6 us less, but all small calls
+// 0.1 to 0.2 us more for the code in between.)
 template <int PER, int W>
 __device__ __forceinline__ void make_plan(const Args &a, Plan *plan, Cursor *place)
 {
@@ -1080,14 +1082,15 @@ int32_t launch(Args &a, int grid, bool f16, void *stream)
 }
 
 // 8-row tiles a warp takes of R query rows, in ceil(R / 8 tiles) passes over a
-// segment.  At 64 segments of 8192 positions (D = 128) a further pass takes 11.8
+// segment.  At 64 segments of 8192 positions (D = 128) a further pass takes 15.7
 // us with one tile; with two, which unpack codes once for both but run 2 warps a
-// scheduler instead of 4, 19.9.  So 24 rows take 52 us in three passes and 56 in
-// two, 40 rows 75 and 76, but 16 rows 39 and 35, 48 rows 87 and 77, and from 6
-// tiles on two a pass are no slower.  (Tiles side by side in a CTA, over one copy
-// of the cache in L2 or shared memory, were no faster when these took 55, 63 and
-// 79 us at 24, 32 and 40 rows: 60, 64 and 93; at 302 MB of cache, past L2, 180,
-// 190 and 286 against 165, 185 and 263.)
+// scheduler instead of 4, 26.5.  So 24 rows take 63 us in three passes and 70 in
+// two, 40 rows 94 and 97, but 16 rows 47 and 43, 48 rows 109 and 98, and from 6
+// tiles on two a pass are no slower (at D = 64: 24 rows 41 and 46, 48 rows 68 and
+// 63, 56 rows 76 and 79).  (Tiles side by side in a CTA, over one copy
+// of the cache in L2 or shared memory, were no faster in an earlier form, when these
+// took 55, 63 and 79 us at 24, 32 and 40 rows: 60, 64 and 93; at 302 MB of cache,
+// past L2, 180, 190 and 286 against 165, 185 and 263.)
 int tiles_of(int R)
 {
     const int t = (R + 7) / 8;

@@ -226,9 +226,9 @@ constexpr int kBlocks = sizeof(E) == 4 ? 5 : 4;
 // One block: a tile of tokens of one head, for every sequence in turn of
 // gridDim.y.  blockDim / (D / 8) rows at a time, ROWS times: 4 where that leaves
 // every SM two full blocks, else 1 (a decode step's few rows finish sooner side
-// by side).  Warps past a sequence's
-// last row read nothing (64 sequences of up to 4096 fp32 rows, one with all and 63
-// with 1: 42 us; 313 where every row was read), and what remains is their launch.
+// by side).  Warps past a sequence's last row read nothing, and what remains is
+// their launch (64 sequences of T = 4096 fp32 rows, one with all and 63 with 1:
+// 42 us; 313 where every row is read).
 template <int D, typename E, int ROWS>
 __global__ void __launch_bounds__(kThreads, kBlocks<E>) append_q4_kernel(const Args a)
 {
